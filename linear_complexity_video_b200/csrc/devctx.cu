@@ -43,6 +43,7 @@ unsigned long long current_context_id()
     const CtxFns &f = ctx_fns();
     if (!f.get_current || !f.get_id) return 0;
     // make sure the runtime has made the device's primary context current
+    CaptureRelaxed relaxed;
     if (cudaFree(nullptr) != cudaSuccess) return 0;
     CUcontext ctx = nullptr;
     if (f.get_current(&ctx) != CUDA_SUCCESS || !ctx) return 0;
