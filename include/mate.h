@@ -59,6 +59,7 @@ extern "C" {
 /* ---- element types ------------------------------------------------------ */
 #define MATE_F32 0  /* x, B, C, q, k, v, out stored as IEEE fp32 */
 #define MATE_BF16 1 /* x, B, C, q, k, v, out stored as bf16; fp32 accumulation */
+#define MATE_I8 2   /* 8-bit codes with one fp32 scale per row (mate_quant_rows_fwd) */
 
 /* ---- Rotary Major Scan orders (paper review, MA-Branch item 2) ----------
  * Scan position n of a T x H x W grid maps to these grid coordinates:
@@ -292,6 +293,126 @@ typedef struct {
 int mate_gate_norm_fwd(const void *y, const void *z, const float *w, float eps, void *out,
                        const mate_gate_norm_dims *d, void *stream);
 
+/* ---- the block in 8 bits ------------------------------------------------- */
+/*
+ * Codes. A row v of K values is held as K signed 8-bit codes and one fp32 scale:
+ *     scale = max_k |v_k| / 127,   q_k = rint(127 v_k / max_k |v_k|)
+ * (ties to even; codes lie in -127 .. 127), so that v_k is about scale * q_k. A
+ * row of zeros has scale 0 and codes 0. A row that holds a NaN or an infinity
+ * has scale NaN and codes 0: whatever is computed from it is NaN.
+ * Activations are held so per token, weights (nn.Linear layout) per output
+ * channel; both by mate_quant_rows_fwd. The pages give no 8-bit form of the
+ * block: this is the common symmetric scheme.
+ */
+typedef struct {
+    int rows;  /* tokens, or output channels of a weight */
+    int k;     /* values per row */
+    int dtype; /* MATE_BF16 (the only storage the kernel takes) */
+} mate_quant_dims;
+
+/*
+ * 8-bit codes and scales of rows (see above). For every row the codes are the
+ * correctly rounded values of the formula.
+ *   x     : (rows, k) bf16, row-major
+ *   q     : (rows, k) int8, row-major
+ *   scale : (rows)    fp32
+ * All pointers device memory; x and q 16-byte aligned, scale 4-byte aligned; q and
+ * scale caller-owned, overlapping neither x nor one another. k a multiple of 8,
+ * k <= 20480, rows > 0. Returns MATE_OK, MATE_ERR_INVALID_ARG (bad pointers, sizes
+ * or overlap), MATE_ERR_UNSUPPORTED (other dtype or sizes) or MATE_ERR_CUDA.
+ */
+int mate_quant_rows_fwd(const void *x, int8_t *q, float *scale, const mate_quant_dims *d, void *stream);
+
+typedef struct {
+    int tokens;    /* rows M */
+    int k;         /* input channels */
+    int n;         /* output channels */
+    int out_dtype; /* MATE_BF16 or MATE_F32: storage of out and addend */
+} mate_linear_i8_dims;
+
+/*
+ * 8-bit linear layer: a product of codes with a scale per token and a scale per
+ * output channel,
+ *     out_mn = x_scale_m w_scale_n sum_k x_mk w_nk (+ bias_n) (+ addend_mn)
+ * with an exact sum (int32), scales, bias and addend in fp32, one rounding to
+ * the output type. The addend serves an output that is the sum of products whose
+ * inputs have scales of their own (the MATE composition of two branches).
+ *   x       : (tokens, k) int8, row-major;  x_scale : (tokens) fp32
+ *   w       : (n, k)      int8, row-major;  w_scale : (n)      fp32
+ *   bias    : (n) fp32 or NULL
+ *   addend  : (tokens, n) out_dtype, row-major, or NULL
+ *   out     : (tokens, n) out_dtype, row-major, caller-owned; may be the addend
+ *             itself (same address), otherwise overlaps no input
+ * All pointers device memory; x_scale 4-byte aligned, the others 16-byte. k a multiple
+ * of 16, k <= 131072; n a multiple of 8; tokens > 0. Results are bitwise
+ * reproducible. Returns MATE_OK, MATE_ERR_INVALID_ARG (bad pointers, sizes or
+ * overlap), MATE_ERR_UNSUPPORTED (other dtype or sizes) or MATE_ERR_CUDA.
+ */
+int mate_linear_i8_fwd(const int8_t *x, const float *x_scale, const int8_t *w, const float *w_scale,
+                       const float *bias, const void *addend, void *out, const mate_linear_i8_dims *d, void *stream);
+
+/*
+ * mate_gate_norm_fwd with its output as 8-bit codes, one scale per row (all
+ * groups of the row together): the same normalised values in fp32, quantised
+ * without a rounding to bf16 between.
+ *   q     : (tokens, channels) int8, row-major, 16-byte aligned
+ *   scale : (tokens) fp32, 4-byte aligned
+ * Both caller-owned, overlapping neither an input nor one another. All else
+ * (y, z, w, eps, sizes, returns) as for mate_gate_norm_fwd.
+ */
+int mate_gate_norm_i8_fwd(const void *y, const void *z, const float *w, float eps, int8_t *q, float *scale,
+                          const mate_gate_norm_dims *d, void *stream);
+
+/* ---- norms around a block ------------------------------------------------ */
+#define MATE_NORM_NONE 0  /* N(v) = v                                   */
+#define MATE_NORM_RMS 1   /* N(v) = v / sqrt(mean v^2 + eps)            */
+#define MATE_NORM_LAYER 2 /* N(v) = (v - mean v) / sqrt(var v + eps)    */
+
+typedef struct {
+    int batch;            /* batch elements, each with its own gate, scale and shift */
+    int tokens;           /* tokens per batch element */
+    int channels;         /* C */
+    int post_norm;        /* MATE_NORM_*: norm of the block's output y */
+    int pre_norm;         /* MATE_NORM_RMS or MATE_NORM_LAYER: norm ahead of the next block */
+    int x_dtype;          /* MATE_BF16 or MATE_F32: storage of x and x_out */
+    int h_dtype;          /* MATE_BF16 or MATE_I8: storage of h */
+    int64_t mod_stride;   /* elements between batch elements in gate, scale and shift */
+    float residual_scale; /* alpha */
+    float eps;
+} mate_block_norm_dims;
+
+/*
+ * The norms before and after a block, with its modulation, its gate and the
+ * residual scale, in one pass over the residual stream x:
+ *     x_out = alpha x + gate_b * (N_post(y) w_post)        when y is given
+ *     h     = N_pre(x_out) w_pre (1 + scale_b) + shift_b   when h is given
+ * with y a block's output and h the next block's input; without y, x_out is not
+ * written and h comes from x itself (ahead of the first block). (Paper review,
+ * section 三: MATE takes the place of self-attention inside the DiT block; the
+ * pages name neither the block's norms nor its modulation, so this is the common
+ * adaLN form.) All arithmetic is fp32 with one rounding per output: h follows
+ * x_out before it is rounded for storage.
+ *   x, x_out    : (batch, tokens, channels) x_dtype, row-major
+ *   y           : (batch, tokens, channels) bf16, row-major
+ *   w_post, w_pre : (channels) fp32, or NULL (ones)
+ *   gate, scale, shift : channels fp32 per batch element, mod_stride elements
+ *                 from one batch element's to the next's (0: all the same), or
+ *                 NULL (gate 1, scale 0, shift 0)
+ *   h           : (batch, tokens, channels) bf16 or int8, row-major
+ *   h_scale     : (batch, tokens) fp32, with int8 h only (codes as above)
+ * y and x_out come together; at least one of y and h is given, and h_scale
+ * exactly when h is int8. x_out may be x itself (same address); otherwise
+ * outputs overlap neither an input nor one another. All pointers device memory;
+ * x, y, x_out and h 16-byte aligned, fp32 vectors 4-byte aligned. channels a
+ * multiple of 8, at most 8192; batch * tokens at most 2^30; eps >= 0 and finite;
+ * residual_scale finite; mod_stride >= 0. Returns MATE_OK, MATE_ERR_INVALID_ARG (bad pointers, sizes,
+ * eps, combinations or overlap), MATE_ERR_UNSUPPORTED (other dtypes, norms or
+ * sizes) or MATE_ERR_CUDA.
+ */
+int mate_block_norm_fwd(const void *x, const void *y, const float *w_post, const float *gate, const float *w_pre,
+                        const float *scale, const float *shift, void *x_out, void *h, float *h_scale,
+                        const mate_block_norm_dims *d, void *stream);
+
 /* ---- MA-branch front-end ------------------------------------------------- */
 typedef struct {
     int batch;
@@ -339,6 +460,21 @@ size_t mate_frontend_workspace_bytes(int T, int H, int W, const mate_frontend_di
 int mate_frontend_fwd(const void *u, const void *w_in, const float *conv_w, const float *conv_b, const float *dt_bias,
                       int T, int H, int W, int scan_mode, void *z, void *x, float *dt, void *B, void *C,
                       const mate_frontend_dims *d, void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * mate_frontend_fwd with in_proj in 8 bits: u and W_in as codes with a scale per
+ * token and per row of W_in, everything after the products as above (they are
+ * rounded to bf16 as there).
+ *   u    : (batch, T, H, W, d_model) int8;  u_scale : (batch, T, H, W) fp32
+ *   w_in : (d_inner + dc + nheads, d_model) int8;  w_scale : (d_inner + dc + nheads) fp32
+ * u and w_in 16-byte aligned, u_scale 4-byte and w_scale 16-byte aligned; d_inner, dc and nheads
+ * multiples of 8, d_model a multiple of 64. All else (dims with dtype MATE_BF16, the storage
+ * of the outputs; workspace; returns) as for mate_frontend_fwd.
+ */
+int mate_frontend_i8_fwd(const int8_t *u, const float *u_scale, const int8_t *w_in, const float *w_scale,
+                         const float *conv_w, const float *conv_b, const float *dt_bias, int T, int H, int W,
+                         int scan_mode, void *z, void *x, float *dt, void *B, void *C, const mate_frontend_dims *d,
+                         void *workspace, size_t ws_bytes, void *stream);
 
 /*
  * Debug export of the scan order the kernels use: out_dev[n] = grid offset
@@ -390,7 +526,10 @@ int mate_last_error(void *stream);
 #define MATE_PHASE_FRONT_PROJ 8  /* mate_frontend_fwd: one in_proj GEMM (3 per call) */
 #define MATE_PHASE_FRONT_CONV 9  /* mate_frontend_fwd: conv along the scan + SiLU   */
 #define MATE_PHASE_FRONT_DT 10   /* mate_frontend_fwd: softplus(dt + bias)          */
-#define MATE_PHASE_GATE_NORM 11  /* mate_gate_norm_fwd                              */
+#define MATE_PHASE_GATE_NORM 11  /* mate_gate_norm_fwd, mate_gate_norm_i8_fwd       */
+#define MATE_PHASE_QUANT_ROWS 12 /* mate_quant_rows_fwd                             */
+#define MATE_PHASE_LINEAR_I8 13  /* mate_linear_i8_fwd's product                    */
+#define MATE_PHASE_BLOCK_NORM 14 /* mate_block_norm_fwd                             */
 
 /*
  * Optional enqueue-time hook, for timing phases with events on the caller's

@@ -20,6 +20,9 @@ MATE_ERR_WORKSPACE = -5
 
 MATE_F32 = 0
 MATE_BF16 = 1
+MATE_I8 = 2
+
+MATE_NORM_NONE, MATE_NORM_RMS, MATE_NORM_LAYER = 0, 1, 2
 
 MATE_DIR_FWD, MATE_DIR_BWD, MATE_DIR_BI = 1, 2, 3
 
@@ -41,12 +44,18 @@ EXPORTS = (
     "mate_frontend_workspace_bytes",
     "mate_frontend_fwd",
     "mate_gate_norm_fwd",
+    "mate_quant_rows_fwd",
+    "mate_linear_i8_fwd",
+    "mate_gate_norm_i8_fwd",
+    "mate_block_norm_fwd",
+    "mate_frontend_i8_fwd",
 )
 
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 PHASES = {1: "review_pool", 2: "review_scan", 3: "chunk_state", 4: "state_pass", 5: "chunk_out", 6: "tesa",
-          7: "compose", 8: "front_proj", 9: "front_conv", 10: "front_dt", 11: "gate_norm"}
+          7: "compose", 8: "front_proj", 9: "front_conv", 10: "front_dt", 11: "gate_norm",
+          12: "quant_rows", 13: "linear_i8", 14: "block_norm"}
 PHASE_HOOK = ctypes.CFUNCTYPE(None, ctypes.c_int, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p)
 
 
@@ -73,6 +82,21 @@ class mate_gate_norm_dims(ctypes.Structure):
 class mate_frontend_dims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int), ("d_model", ctypes.c_int), ("nheads", ctypes.c_int), ("headdim", ctypes.c_int),
                 ("ngroups", ctypes.c_int), ("dstate", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class mate_quant_dims(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int), ("k", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
+class mate_linear_i8_dims(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int), ("k", ctypes.c_int), ("n", ctypes.c_int), ("out_dtype", ctypes.c_int)]
+
+
+class mate_block_norm_dims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("tokens", ctypes.c_int), ("channels", ctypes.c_int),
+                ("post_norm", ctypes.c_int), ("pre_norm", ctypes.c_int), ("x_dtype", ctypes.c_int),
+                ("h_dtype", ctypes.c_int), ("mod_stride", ctypes.c_int64), ("residual_scale", ctypes.c_float),
+                ("eps", ctypes.c_float)]
 
 
 class MateError(RuntimeError):
@@ -120,6 +144,17 @@ def load() -> ctypes.CDLL:
     L.mate_frontend_fwd.argtypes = [_vp] * 5 + [ctypes.c_int] * 4 + [_vp] * 5 + [ctypes.POINTER(mate_frontend_dims),
                                                                             _vp, ctypes.c_size_t, _vp]
     L.mate_frontend_fwd.restype = ctypes.c_int
+    L.mate_frontend_i8_fwd.argtypes = [_vp] * 7 + [ctypes.c_int] * 4 + [_vp] * 5 + [ctypes.POINTER(mate_frontend_dims),
+                                                                               _vp, ctypes.c_size_t, _vp]
+    L.mate_frontend_i8_fwd.restype = ctypes.c_int
+    L.mate_quant_rows_fwd.argtypes = [_vp] * 3 + [ctypes.POINTER(mate_quant_dims), _vp]
+    L.mate_quant_rows_fwd.restype = ctypes.c_int
+    L.mate_linear_i8_fwd.argtypes = [_vp] * 7 + [ctypes.POINTER(mate_linear_i8_dims), _vp]
+    L.mate_linear_i8_fwd.restype = ctypes.c_int
+    L.mate_gate_norm_i8_fwd.argtypes = [_vp] * 3 + [ctypes.c_float, _vp, _vp, ctypes.POINTER(mate_gate_norm_dims), _vp]
+    L.mate_gate_norm_i8_fwd.restype = ctypes.c_int
+    L.mate_block_norm_fwd.argtypes = [_vp] * 10 + [ctypes.POINTER(mate_block_norm_dims), _vp]
+    L.mate_block_norm_fwd.restype = ctypes.c_int
     L.mate_version.argtypes = []
     L.mate_version.restype = ctypes.c_int
     L.mate_set_phase_hook.argtypes = [PHASE_HOOK, ctypes.c_void_p]

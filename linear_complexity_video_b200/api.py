@@ -9,13 +9,15 @@ dims off the tensor shapes and allocate the output and workspace with torch.
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Sequence
+from contextlib import contextmanager
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
 from . import _lib
-from ._lib import (MATE_BF16, MATE_DIR_BI, MATE_F32, check, mate_attn_dims, mate_compose_dims, mate_frontend_dims,
-                   mate_gate_norm_dims, mate_ssd_dims)
+from ._lib import (MATE_BF16, MATE_DIR_BI, MATE_F32, MATE_I8, MATE_NORM_LAYER, MATE_NORM_NONE, MATE_NORM_RMS, check,
+                   mate_attn_dims, mate_block_norm_dims, mate_compose_dims, mate_frontend_dims, mate_gate_norm_dims,
+                   mate_linear_i8_dims, mate_quant_dims, mate_ssd_dims)
 
 _DT = {torch.float32: MATE_F32, torch.bfloat16: MATE_BF16}
 
@@ -45,6 +47,52 @@ def _require(t: torch.Tensor, name: str, dtype=None):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+class Codes(NamedTuple):
+    """Rows held as 8-bit codes: value[..., k] is about q[..., k] * scale[...]."""
+    q: torch.Tensor      # (..., K) int8
+    scale: torch.Tensor  # (...) fp32
+
+
+@contextmanager
+def _on(t: torch.Tensor, stream):
+    """`t`'s device and `stream` made current, so that outputs and temporaries belong to
+    the stream that writes them. Yields the stream handle of the call."""
+    with torch.cuda.device(t.device):
+        if stream is None:
+            yield torch.cuda.current_stream(t.device)
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            handle = int(getattr(stream, "cuda_stream", stream))
+            stream = torch.cuda.ExternalStream(handle, device=t.device) if handle else torch.cuda.default_stream(t.device)
+        if stream.device != t.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+        with torch.cuda.stream(stream):
+            yield stream
+
+
+def _same_device(first: torch.Tensor, **others):
+    for n, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{n} must be on {first.device}, got {t.device}")
+
+
+def _rows(shape) -> int:
+    n = 1
+    for s in shape:
+        n *= int(s)
+    return n
+
+
+def _out(out: Optional[torch.Tensor], name: str, shape, dtype, like: torch.Tensor) -> torch.Tensor:
+    if out is None:
+        return torch.empty(*shape, dtype=dtype, device=like.device)
+    _require(out, name, dtype)
+    if tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(out.shape)}")
+    _same_device(like, **{name: out})
+    return out
 
 
 def ssd_dims(batch, nheads, headdim, dstate, ngroups, chunk, dtype, directions=MATE_DIR_BI) -> mate_ssd_dims:
@@ -97,6 +145,31 @@ def mate_gate_norm_fwd(y, z, w, eps: float, out, dims: mate_gate_norm_dims, stre
     rc = _lib.load().mate_gate_norm_fwd(_ptr(y), _ptr(z), _ptr(w), float(eps), _ptr(out), ctypes.byref(dims),
                                         _stream_handle(stream))
     check("mate_gate_norm_fwd", rc)
+
+
+def mate_quant_rows_fwd(x, q, scale, dims: mate_quant_dims, stream=None) -> None:
+    rc = _lib.load().mate_quant_rows_fwd(_ptr(x), _ptr(q), _ptr(scale), ctypes.byref(dims), _stream_handle(stream))
+    check("mate_quant_rows_fwd", rc)
+
+
+def mate_linear_i8_fwd(x, x_scale, w, w_scale, bias, addend, out, dims: mate_linear_i8_dims, stream=None) -> None:
+    rc = _lib.load().mate_linear_i8_fwd(_ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(bias), _ptr(addend),
+                                        _ptr(out), ctypes.byref(dims), _stream_handle(stream))
+    check("mate_linear_i8_fwd", rc)
+
+
+def mate_gate_norm_i8_fwd(y, z, w, eps: float, q, scale, dims: mate_gate_norm_dims, stream=None) -> None:
+    rc = _lib.load().mate_gate_norm_i8_fwd(_ptr(y), _ptr(z), _ptr(w), float(eps), _ptr(q), _ptr(scale),
+                                           ctypes.byref(dims), _stream_handle(stream))
+    check("mate_gate_norm_i8_fwd", rc)
+
+
+def mate_block_norm_fwd(x, y, w_post, gate, w_pre, scale, shift, x_out, h, h_scale, dims: mate_block_norm_dims,
+                        stream=None) -> None:
+    rc = _lib.load().mate_block_norm_fwd(_ptr(x), _ptr(y), _ptr(w_post), _ptr(gate), _ptr(w_pre), _ptr(scale),
+                                         _ptr(shift), _ptr(x_out), _ptr(h), _ptr(h_scale), ctypes.byref(dims),
+                                         _stream_handle(stream))
+    check("mate_block_norm_fwd", rc)
 
 
 def mate_debug_rms_map(T, H, W, scan_mode, flip, out, stream=None) -> None:
@@ -215,6 +288,155 @@ def linear(x, w, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tenso
     return out
 
 
+def quantize_rows(x, stream=None) -> Codes:
+    """8-bit codes and the scale of every row. x: (..., K) bf16, tokens or the rows of an
+    nn.Linear weight. Returns Codes(q (..., K) int8, scale (...) fp32) with
+    scale = max|x| / 127 and q = rint(127 x / max|x|)."""
+    _require(x, "x", torch.bfloat16)
+    with _on(x, stream) as st:
+        q = torch.empty_like(x, dtype=torch.int8)
+        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        mate_quant_rows_fwd(x, q, scale, mate_quant_dims(_rows(x.shape[:-1]), int(x.shape[-1]), MATE_BF16), st)
+    return Codes(q, scale)
+
+
+def linear_i8(x_q, x_scale, w_q, w_scale, bias=None, addend=None, out_dtype=torch.bfloat16,
+              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """8-bit linear layer: x_scale w_scale (x_q w_q^T) + bias + addend, the sum exact and one
+    rounding to out_dtype (bf16 or fp32). x_q: (..., K) int8; x_scale: (...) fp32; w_q: (N, K)
+    int8; w_scale: (N,) fp32; bias: (N,) fp32; addend: (..., N) out_dtype, and may be `out`.
+    Returns (..., N)."""
+    if out_dtype not in _DT:
+        raise ValueError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
+    _require(x_q, "x_q", torch.int8)
+    _require(w_q, "w_q", torch.int8)
+    _require(x_scale, "x_scale", torch.float32)
+    _require(w_scale, "w_scale", torch.float32)
+    if w_q.dim() != 2 or x_q.dim() < 1 or x_q.shape[-1] != w_q.shape[1]:
+        raise ValueError("x_q must be (..., K) and w_q (N, K)")
+    lead, N = tuple(x_q.shape[:-1]), int(w_q.shape[0])
+    if tuple(x_scale.shape) != lead or tuple(w_scale.shape) != (N,):
+        raise ValueError("x_scale must have one entry per token and w_scale one per row of w_q")
+    if bias is not None:
+        _require(bias, "bias", torch.float32)
+        if tuple(bias.shape) != (N,):
+            raise ValueError("bias must have one entry per row of w_q")
+    if addend is not None:
+        _require(addend, "addend", out_dtype)
+        if tuple(addend.shape) != lead + (N,):
+            raise ValueError(f"addend must have shape {lead + (N,)}")
+    _same_device(x_q, x_scale=x_scale, w_q=w_q, w_scale=w_scale, bias=bias, addend=addend)
+    with _on(x_q, stream) as st:
+        out = _out(out, "out", lead + (N,), out_dtype, x_q)
+        dims = mate_linear_i8_dims(_rows(lead), int(x_q.shape[-1]), N, _DT[out_dtype])
+        mate_linear_i8_fwd(x_q, x_scale, w_q, w_scale, bias, addend, out, dims, st)
+    return out
+
+
+def gate_norm_i8(y, z, w, group: int, eps: float = 1e-5, stream=None) -> Codes:
+    """gate_norm with its output as 8-bit codes and one scale per row (not rounded to bf16
+    between). Arguments as for gate_norm. Returns Codes(q (..., C), scale (...))."""
+    _require(y, "y", torch.bfloat16)
+    _require(z, "z", torch.bfloat16)
+    _require(w, "w", torch.float32)
+    if z.shape != y.shape or w.shape != (y.shape[-1],):
+        raise ValueError("y and z must have one shape and w one entry per channel")
+    _same_device(y, z=z, w=w)
+    with _on(y, stream) as st:
+        q = torch.empty_like(y, dtype=torch.int8)
+        scale = torch.empty(y.shape[:-1], dtype=torch.float32, device=y.device)
+        dims = mate_gate_norm_dims(_rows(y.shape[:-1]), int(y.shape[-1]), int(group), MATE_BF16)
+        mate_gate_norm_i8_fwd(y, z, w, eps, q, scale, dims, st)
+    return Codes(q, scale)
+
+
+_NORMS = {"rms": MATE_NORM_RMS, "layer": MATE_NORM_LAYER}
+
+
+def block_norm(x, y=None, *, w_post=None, gate=None, residual_scale: float = 1.0, post_norm: bool = True, w_pre=None,
+               scale=None, shift=None, norm: str = "rms", eps: float = 1e-6, h_dtype=torch.bfloat16,
+               x_out: Optional[torch.Tensor] = None, stream=None):
+    """The norms before and after a block with its modulation, gate and residual scale, in
+    one pass over the residual stream:
+        x_out = residual_scale x + gate (N(y) w_post)     with y, the block's output
+        h     = N(x_out) w_pre (1 + scale) + shift        the next block's input
+    (h from x itself without y). x: (batch, ..., C) bf16 or fp32; y: like x, bf16; w_post,
+    w_pre: (C,) fp32; gate, scale, shift: (batch, C) fp32 (or (C,) for all batch elements), which
+    may be column ranges of one wider tensor. norm: "rms" or "layer", for both norms;
+    post_norm=False leaves y as it is. h_dtype: torch.bfloat16, torch.int8 (h is Codes) or None
+    (no h). x_out may be x. Returns (x_out or None, h or None)."""
+    if norm not in _NORMS:
+        raise ValueError(f"norm must be one of {sorted(_NORMS)}, got {norm!r}")
+    if h_dtype not in (torch.bfloat16, torch.int8, None):
+        raise ValueError(f"h_dtype must be bfloat16, int8 or None, got {h_dtype}")
+    if y is None and (w_post is not None or gate is not None or x_out is not None or residual_scale != 1.0):
+        raise ValueError("w_post, gate, residual_scale and x_out go with y")
+    if h_dtype is None and (w_pre is not None or scale is not None or shift is not None):
+        raise ValueError("w_pre, scale and shift go with h")
+    if y is None and h_dtype is None:
+        raise ValueError("nothing to compute: neither y nor h")
+    _require(x, "x")
+    if x.dtype not in _DT or x.dim() < 2:
+        raise ValueError(f"x must be (batch, ..., C) bfloat16 or float32, got {x.dtype}")
+    batch, C = int(x.shape[0]), int(x.shape[-1])
+    if y is not None:
+        _require(y, "y", torch.bfloat16)
+        if y.shape != x.shape:
+            raise ValueError("x and y must have one shape")
+    for t, n in ((w_post, "w_post"), (w_pre, "w_pre")):
+        if t is not None:
+            _require(t, n, torch.float32)
+            if tuple(t.shape) != (C,):
+                raise ValueError(f"{n} must have one entry per channel")
+    mod_stride = None
+    for t, n in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32:
+            raise ValueError(f"{n} must be a float32 CUDA tensor")
+        if tuple(t.shape) not in ((batch, C), (C,)) or (C > 1 and t.stride(-1) != 1):
+            raise ValueError(f"{n} must be (batch, C) or (C,), its channels contiguous")
+        s = 0 if t.dim() == 1 or batch == 1 else int(t.stride(0))
+        if mod_stride not in (None, s):
+            raise ValueError("gate, scale and shift must have one stride between batch elements")
+        mod_stride = s
+    _same_device(x, y=y, w_post=w_post, gate=gate, w_pre=w_pre, scale=scale, shift=shift, x_out=x_out)
+    with _on(x, stream) as st:
+        h = h_scale = None
+        if y is not None:
+            x_out = _out(x_out, "x_out", x.shape, x.dtype, x)
+        if h_dtype is not None:
+            h = torch.empty(x.shape, dtype=h_dtype, device=x.device)
+            if h_dtype == torch.int8:
+                h_scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        dims = mate_block_norm_dims(batch, _rows(x.shape[1:-1]), C, _NORMS[norm] if post_norm else MATE_NORM_NONE,
+                                    _NORMS[norm], _DT[x.dtype], MATE_I8 if h_dtype == torch.int8 else MATE_BF16,
+                                    mod_stride or 0, float(residual_scale), float(eps))
+        mate_block_norm_fwd(x, y, w_post, gate, w_pre, scale, shift, x_out, h, h_scale, dims, st)
+    return x_out, (Codes(h, h_scale) if h_scale is not None else h)
+
+
+# the block's weights that its matrix products read
+_PROJECTIONS = ("w_in", "w_q", "w_k", "w_v", "w_ma", "w_te")
+
+
+def quantize_block(weights, stream=None):
+    """A block's weights with those of its matrix products as 8-bit codes (a scale per output
+    channel), for block() and stack(). The others are kept as they are."""
+    out = dict(weights)
+    for n in _PROJECTIONS:
+        out[n] = quantize_rows(weights[n], stream=stream)
+    return out
+
+
+def modulation(c, w: Codes, bias=None, stream=None) -> torch.Tensor:
+    """A layer's modulation vectors from its conditioning, as an 8-bit linear layer with fp32
+    output. c: (batch, K) bf16; w: Codes of (3 d_model, K); bias: (3 d_model,) fp32. Returns
+    (batch, 3 d_model): shift, scale and gate, as stack() takes them."""
+    x = quantize_rows(c, stream=stream)
+    return linear_i8(x.q, x.scale, w.q, w.scale, bias=bias, out_dtype=torch.float32, stream=stream)
+
+
 def block(u, weights, *, scan_mode: int, review_pool, chunk: int, nheads: int, headdim: int, ngroups: int,
           dstate: int, attn_heads: int, attn_dim: int, Tw: int, Sw: int, shift, eps: float = 1e-5, stream=None,
           keep: bool = False):
@@ -225,8 +447,14 @@ def block(u, weights, *, scan_mode: int, review_pool, chunk: int, nheads: int, h
         out = y_ma w_ma^T + y_te w_te^T
     weights: w_in, conv_w, conv_b, dt_bias, A, D, norm_w, w_q, w_k, w_v, w_ma, w_te (as
     workloads.generate_block draws them). Returns out (batch, T, H, W, d_model), and with
-    `keep` also a dict of the intermediate tensors."""
+    `keep` also a dict of the intermediate tensors.
+    With weights from quantize_block every matrix product runs in 8 bits: u may then be Codes (a
+    block_norm's h) and is quantised per token otherwise, the gated norm and the TESA output
+    become Codes too, and the scan and the attention run in bf16 as above."""
     w = weights
+    if isinstance(w["w_in"], Codes):
+        return _block_i8(u, w, scan_mode, review_pool, chunk, nheads, headdim, ngroups, dstate, attn_heads, attn_dim, Tw,
+                         Sw, shift, eps, stream, keep)
     b, T, H, W, _ = u.shape
     z, x, dt, B, C = frontend(u, w["w_in"], w["conv_w"], w["conv_b"], w["dt_bias"], scan_mode, nheads, headdim,
                               ngroups, dstate, stream=stream)
@@ -239,6 +467,59 @@ def block(u, weights, *, scan_mode: int, review_pool, chunk: int, nheads: int, h
     if keep:
         return out, dict(z=z, x=x, dt=dt, B=B, C=C, y=y, y_ma=y_ma, q=q, k=k, v=v, y_te=y_te)
     return out
+
+
+def _block_i8(u, w, scan_mode, review_pool, chunk, nheads, headdim, ngroups, dstate, attn_heads, attn_dim, Tw, Sw, shift,
+              eps, stream, keep):
+    if not isinstance(u, Codes):
+        u = quantize_rows(u, stream=stream)
+    with _on(u.q, stream) as st:
+        b, T, H, W, _ = u.q.shape
+        z, x, dt, B, C = frontend_i8(u, w["w_in"], w["conv_w"], w["conv_b"], w["dt_bias"], scan_mode, nheads, headdim,
+                                     ngroups, dstate, stream=st)
+        y = bissd(x, dt, w["A"], B, C, w["D"], scan_mode, review_pool, chunk=chunk, stream=st)
+        d_inner = nheads * headdim
+        y_ma = gate_norm_i8(y.view(b, T, H, W, d_inner), z, w["norm_w"], d_inner // ngroups, eps, stream=st)
+        q, k, v = (linear_i8(*u, *w[n], stream=st).view(b, T, H, W, attn_heads, attn_dim) for n in ("w_q", "w_k", "w_v"))
+        y_te = tesa(q, k, v, Tw, Sw, shift, stream=st)
+        c_te = quantize_rows(y_te.view(b, T, H, W, attn_heads * attn_dim), stream=st)
+        # the branches' codes have scales of their own: the second product adds the first
+        out = linear_i8(*c_te, *w["w_te"], stream=st)
+        linear_i8(*y_ma, *w["w_ma"], addend=out, out=out, stream=st)
+    if keep:
+        return out, dict(u=u, z=z, x=x, dt=dt, B=B, C=C, y=y, y_ma=y_ma, q=q, k=k, v=v, y_te=y_te, c_te=c_te)
+    return out
+
+
+def stack(x, layers, *, norm: str = "rms", residual_scale: float = 1.0, norm_eps: float = 1e-6, stream=None, **spec):
+    """Residual layers around the token mixer (adaLN form). For each layer in turn, with N the
+    norm and (shift, scale, gate) its modulation:
+        h = N(x) w_pre (1 + scale) + shift;  y = block(h);  x = residual_scale x + gate N(y) w_post
+    x: (batch, T, H, W, d_model) bf16 or fp32, not written. layers: a sequence of (weights, mod) or
+    (weights, mod, overrides): weights as block() takes them (8-bit ones run the layer in 8 bits), with
+    w_pre and w_post (d_model,) fp32 where the norms have weights; mod (batch, 3 d_model) fp32, the
+    shift, scale and gate of every batch element (see modulation()); overrides a dict of block()
+    arguments of that layer alone (scan_mode and shift alternate between layers). spec: block()'s
+    arguments. The norm after a layer and the one before the next are one pass. Returns x."""
+    layers = [tuple(ly) + ({},) * (3 - len(ly)) for ly in layers]
+    if not layers:
+        return x
+    with _on(x, stream) as st:
+        C = int(x.shape[-1])
+        kw = dict(norm=norm, eps=norm_eps, stream=st)
+
+        def pre(ly):
+            w, mod, _ = ly
+            return dict(w_pre=w.get("w_pre"), shift=mod[:, :C], scale=mod[:, C:2 * C],
+                        h_dtype=torch.int8 if isinstance(w["w_in"], Codes) else torch.bfloat16)
+
+        _, h = block_norm(x, **pre(layers[0]), **kw)
+        for i, (w, mod, over) in enumerate(layers):
+            y = block(h, w, stream=st, **{**spec, **over})
+            after = pre(layers[i + 1]) if i + 1 < len(layers) else dict(h_dtype=None)
+            x, h = block_norm(x, y, w_post=w.get("w_post"), gate=mod[:, 2 * C:], residual_scale=residual_scale, **after,
+                              **kw)
+    return x
 
 
 def mate_frontend_workspace_bytes(T: int, H: int, W: int, dims: mate_frontend_dims) -> int:
@@ -276,6 +557,50 @@ def frontend(u, w_in, conv_w, conv_b, dt_bias, scan_mode: int, nheads: int, head
     Bm = torch.empty(b, T, H, W, ngroups, dstate, **kw)
     Cm = torch.empty(b, T, H, W, ngroups, dstate, **kw)
     mate_frontend_fwd(u, w_in, conv_w, conv_b, dt_bias, T, H, W, scan_mode, z, x, dt, Bm, Cm, dims, ws, stream)
+    return z, x, dt, Bm, Cm
+
+
+def mate_frontend_i8_fwd(u, u_scale, w_in, w_scale, conv_w, conv_b, dt_bias, T, H, W, scan_mode, z, x, dt, B, C,
+                         dims: mate_frontend_dims, workspace, stream=None) -> None:
+    nbytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    rc = _lib.load().mate_frontend_i8_fwd(_ptr(u), _ptr(u_scale), _ptr(w_in), _ptr(w_scale), _ptr(conv_w),
+                                          _ptr(conv_b), _ptr(dt_bias), T, H, W, scan_mode, _ptr(z), _ptr(x), _ptr(dt),
+                                          _ptr(B), _ptr(C), ctypes.byref(dims), _ptr(workspace), nbytes,
+                                          _stream_handle(stream))
+    check("mate_frontend_i8_fwd", rc)
+
+
+def frontend_i8(u: Codes, w_in: Codes, conv_w, conv_b, dt_bias, scan_mode: int, nheads: int, headdim: int, ngroups: int,
+                dstate: int, stream=None):
+    """frontend with in_proj in 8 bits. u: Codes of (batch, T, H, W, d_model); w_in: Codes of
+    (d_inner + dc + nheads, d_model); the rest and the results as for frontend."""
+    _require(u.q, "u.q", torch.int8)
+    _require(w_in.q, "w_in.q", torch.int8)
+    for t, n in ((u.scale, "u.scale"), (w_in.scale, "w_in.scale"), (conv_w, "conv_w"), (conv_b, "conv_b"),
+                 (dt_bias, "dt_bias")):
+        _require(t, n, torch.float32)
+    b, T, H, W, dm = u.q.shape
+    d_inner, dc = nheads * headdim, nheads * headdim + 2 * ngroups * dstate
+    for t, n, shape in ((u.scale, "u.scale", (b, T, H, W)), (w_in.q, "w_in.q", (d_inner + dc + nheads, dm)),
+                        (w_in.scale, "w_in.scale", (d_inner + dc + nheads,)), (conv_w, "conv_w", (dc, 4)),
+                        (conv_b, "conv_b", (dc,)), (dt_bias, "dt_bias", (nheads,))):
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{n} must have shape {shape}, got {tuple(t.shape)}")
+    _same_device(u.q, u_scale=u.scale, w_in=w_in.q, w_scale=w_in.scale, conv_w=conv_w, conv_b=conv_b, dt_bias=dt_bias)
+    dims = mate_frontend_dims(b, dm, nheads, headdim, ngroups, dstate, MATE_BF16)
+    nbytes = mate_frontend_workspace_bytes(T, H, W, dims)
+    if nbytes == 0:
+        raise ValueError("unsupported front-end dims")
+    with _on(u.q, stream) as st:
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=u.q.device)
+        kw = dict(dtype=torch.bfloat16, device=u.q.device)
+        z = torch.empty(b, T, H, W, d_inner, **kw)
+        x = torch.empty(b, T, H, W, nheads, headdim, **kw)
+        dt = torch.empty(b, T, H, W, nheads, dtype=torch.float32, device=u.q.device)
+        Bm = torch.empty(b, T, H, W, ngroups, dstate, **kw)
+        Cm = torch.empty(b, T, H, W, ngroups, dstate, **kw)
+        mate_frontend_i8_fwd(u.q, u.scale, w_in.q, w_in.scale, conv_w, conv_b, dt_bias, T, H, W, scan_mode, z, x, dt,
+                             Bm, Cm, dims, ws, st)
     return z, x, dt, Bm, Cm
 
 

@@ -179,19 +179,35 @@ cudaError_t launch_front(const FrontArgs &a, cudaStream_t s)
     const int ns[3] = {a.d_inner, a.dc, a.nh};
     size_t row0 = 0;
     for (int i = 0; i < 3; ++i) {
-        ComposeArgs g = {};
-        g.y1 = a.u;
-        g.w1 = w + row0 * a.d_model;
-        g.y2 = nullptr;
-        g.w2 = nullptr;
-        g.out = const_cast<void *>(outs[i]);
-        g.M = (int)M;
-        g.N = ns[i];
-        g.K1 = a.d_model;
-        g.K2 = 0;
-        g.phase = MATE_PHASE_FRONT_PROJ;
-        g.err = a.err;
-        cudaError_t e = launch_compose_tc(g, s);
+        cudaError_t e;
+        if (a.u_scale) {
+            LinearI8Args g = {};
+            g.x = static_cast<const int8_t *>(a.u);
+            g.w = static_cast<const int8_t *>(a.w_in) + row0 * a.d_model;
+            g.x_scale = a.u_scale;
+            g.w_scale = a.w_scale + row0;
+            g.out = const_cast<void *>(outs[i]);
+            g.M = (int)M;
+            g.N = ns[i];
+            g.K = a.d_model;
+            g.phase = MATE_PHASE_FRONT_PROJ;
+            g.err = a.err;
+            e = launch_linear_i8(g, s);
+        } else {
+            ComposeArgs g = {};
+            g.y1 = a.u;
+            g.w1 = w + row0 * a.d_model;
+            g.y2 = nullptr;
+            g.w2 = nullptr;
+            g.out = const_cast<void *>(outs[i]);
+            g.M = (int)M;
+            g.N = ns[i];
+            g.K1 = a.d_model;
+            g.K2 = 0;
+            g.phase = MATE_PHASE_FRONT_PROJ;
+            g.err = a.err;
+            e = launch_compose_tc(g, s);
+        }
         if (e != cudaSuccess) return e;
         row0 += ns[i];
     }

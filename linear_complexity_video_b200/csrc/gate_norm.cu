@@ -14,6 +14,7 @@
 // The sums of squares go per vector to shared memory, warp w reduces groups
 // w, w + 4, ... there, and each thread scales its vectors by its groups' factors.
 #include "common.cuh"
+#include "i8.cuh"
 #include "kernels.h"
 #include "tc.cuh"
 
@@ -30,8 +31,11 @@ constexpr int kGnMaxVec = 8;  // vectors per thread: rows of up to 8 x 8 x 128 =
 // far below the bf16 rounding of the result, for either sign of v)
 __device__ __forceinline__ float silu_fast(float v) { return __fdividef(v, 1.f + __expf(-v)); }
 
-__global__ void __launch_bounds__(kGnThreads) gate_norm_kernel(GateNormArgs a)
+// I8: the output row as 8-bit codes and a scale (i8.cuh) instead of bf16: one more
+// pass over the registers for the row's largest magnitude
+template <bool I8> __global__ void __launch_bounds__(kGnThreads) gate_norm_kernel(GateNormArgs a)
 {
+    __shared__ uint32_t amax[kGnThreads / 32];
     __shared__ float ss_vec[kGnMaxVec * kGnThreads];  // sum of squares of each vector of the row
     __shared__ float scale[kGnMaxVec * kGnThreads];   // 1 / rms of each group (at most one per vector)
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -77,6 +81,7 @@ __global__ void __launch_bounds__(kGnThreads) gate_norm_kernel(GateNormArgs a)
     }
     __syncthreads();
     uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + row);
+    float m = 0.f;
     const float4 *w4 = reinterpret_cast<const float4 *>(a.w);
 #pragma unroll
     for (int j = 0; j < kGnMaxVec; ++j) {
@@ -85,12 +90,42 @@ __global__ void __launch_bounds__(kGnThreads) gate_norm_kernel(GateNormArgs a)
             const float f = scale[v / gv];
             const float4 wa = w4[2 * v], wb = w4[2 * v + 1];
             const float wv[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
-            uint32_t o[4];
+            if constexpr (I8) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                o[e] = tc::pack_bf16(g[j][2 * e] * f * wv[2 * e], g[j][2 * e + 1] * f * wv[2 * e + 1]);
-            out[v] = make_uint4(o[0], o[1], o[2], o[3]);
+                for (int e = 0; e < 8; ++e) {
+                    g[j][e] = g[j][e] * f * wv[e];
+                    m = i8::amax_nan(m, g[j][e]);
+                }
+            } else {
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[e] = tc::pack_bf16(g[j][2 * e] * f * wv[2 * e], g[j][2 * e + 1] * f * wv[2 * e + 1]);
+                out[v] = make_uint4(o[0], o[1], o[2], o[3]);
+            }
         }
+    }
+    if constexpr (I8) {
+        uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+        if (lane == 0) amax[warp] = mb;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kGnThreads / 32; ++i) mb = max(mb, amax[i]);
+        const i8::RowScale rs = i8::row_scale(__uint_as_float(mb));
+        uint2 *q = reinterpret_cast<uint2 *>(a.q + row);
+#pragma unroll
+        for (int j = 0; j < kGnMaxVec; ++j) {
+            const int v = t + j * kGnThreads;
+            if (v < nv) {
+                if (rs.pre != 1.f) {  // zero, tiny or not finite (where 0 * v would be NaN)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) g[j][e] = rs.pre == 0.f ? 0.f : g[j][e] * rs.pre;
+                }
+                q[v] = make_uint2(i8::codes4(g[j][0], g[j][1], g[j][2], g[j][3], rs.mul),
+                                  i8::codes4(g[j][4], g[j][5], g[j][6], g[j][7], rs.mul));
+            }
+        }
+        if (t == 0) a.scale[blockIdx.x] = rs.scale;
     }
 }
 
@@ -105,7 +140,10 @@ bool gate_norm_supported(const GateNormArgs &a)
 cudaError_t launch_gate_norm(const GateNormArgs &a, cudaStream_t s)
 {
     Phase ph(MATE_PHASE_GATE_NORM, s);
-    gate_norm_kernel<<<a.M, kGnThreads, 0, s>>>(a);
+    if (a.q)
+        gate_norm_kernel<true><<<a.M, kGnThreads, 0, s>>>(a);
+    else
+        gate_norm_kernel<false><<<a.M, kGnThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 

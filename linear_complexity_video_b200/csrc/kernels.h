@@ -106,7 +106,8 @@ struct ComposeArgs {
 // MA-branch front-end (mate_frontend_fwd): in_proj, causal conv along the scan
 // order, SiLU, softplus(dt + bias). dc = d_inner + 2 G Ns conv channels.
 struct FrontArgs {
-    const void *u, *w_in;                 // (batch*N, d_model), (d_inner + dc + nh, d_model) bf16
+    const void *u, *w_in;                 // (batch*N, d_model), (d_inner + dc + nh, d_model) bf16, or 8-bit codes
+    const float *u_scale, *w_scale;       // with codes: (batch*N), (d_inner + dc + nh); null with bf16
     const float *conv_w, *conv_b, *dt_bias;  // (dc, 4), (dc), (nh)
     void *z, *x, *B, *C;                  // outputs, grid order, bf16
     float *dt;                            // (batch*N, nh) fp32
@@ -122,9 +123,47 @@ struct FrontArgs {
 struct GateNormArgs {
     const void *y, *z;
     const float *w;
-    void *out;
+    void *out;               // null when q is set
+    int8_t *q;               // 8-bit codes (M, C) and their row scales (M), instead of out
+    float *scale;
     int M, C, group;
     float eps;
+};
+
+// 8-bit row quantisation (mate_quant_rows_fwd). x: (M, K) bf16; q: (M, K); scale: (M).
+struct QuantArgs {
+    const void *x;
+    int8_t *q;
+    float *scale;
+    int M, K;
+};
+
+// 8-bit linear layer (mate_linear_i8_fwd): out (M x N) = x_scale[m] w_scale[n] sum_k
+// x (M x K) w (N x K) + bias[n] + addend[m, n]; out and addend bf16 or fp32.
+struct LinearI8Args {
+    const int8_t *x, *w;
+    const float *x_scale, *w_scale, *bias;
+    const void *addend;
+    void *out;
+    int M, N, K;
+    int out_f32;
+    int phase;               // MATE_PHASE_* reported for the launch (0: MATE_PHASE_LINEAR_I8)
+    int *err;                // device error word
+};
+
+// Norms around a block (mate_block_norm_fwd): r = alpha x + gate N(y) w_post,
+// h = N(r) w_pre (1 + scale) + shift. Rows (batch, n), C channels.
+struct BlockNormArgs {
+    const void *x, *y;       // (batch, n, C): fp32 or bf16; bf16
+    const float *w_post, *gate, *w_pre, *scale, *shift;  // (C); (batch, C) rows mod_stride apart
+    void *x_out, *h;
+    float *h_scale;
+    int batch, n, C;
+    int post, pre;           // MATE_NORM_*
+    int x_f32;
+    int h_type;              // MATE_BF16, MATE_F32 or MATE_I8
+    int64_t mod_stride;
+    float alpha, eps;
 };
 
 // Phase hook and launch counter (mate_set_phase_hook / mate_kernel_launches).
@@ -166,6 +205,12 @@ bool front_supported(const FrontArgs &a);
 cudaError_t launch_front(const FrontArgs &a, cudaStream_t s);
 bool gate_norm_supported(const GateNormArgs &a);
 cudaError_t launch_gate_norm(const GateNormArgs &a, cudaStream_t s);
+bool quant_rows_supported(const QuantArgs &a);
+cudaError_t launch_quant_rows(const QuantArgs &a, cudaStream_t s);
+bool linear_i8_supported(const LinearI8Args &a);
+cudaError_t launch_linear_i8(const LinearI8Args &a, cudaStream_t s);
+bool block_norm_supported(const BlockNormArgs &a);
+cudaError_t launch_block_norm(const BlockNormArgs &a, cudaStream_t s);
 // tensor-core bi-SSD path (bf16, head dim 64, d_state 64, both directions)
 bool ssd_tc_supported(const SsdArgs &a);
 cudaError_t launch_ssd_tc(const SsdArgs &a, cudaStream_t s);

@@ -35,6 +35,7 @@ int *error_word_ptr()
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
     const unsigned long long ctx = current_context_id();
     std::lock_guard<std::mutex> lock(mu);
+    CaptureRelaxed relaxed;
     if (!addr[dev] || ctx != ctx_of[dev]) {
         void *p = nullptr;
         if (cudaGetSymbolAddress(&p, g_error_word) != cudaSuccess) return nullptr;
@@ -66,6 +67,24 @@ bool overlaps(const void *a, size_t na, const void *b, size_t nb)
 {
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
     return a0 < b0 + nb && b0 < a0 + na;
+}
+
+struct Range {
+    const void *p;
+    size_t n;  // bytes; 0: no such tensor
+};
+
+// every output disjoint from every input and from the other outputs
+bool disjoint(const Range *outs, int no, const Range *ins, int ni)
+{
+    for (int i = 0; i < no; ++i) {
+        if (!outs[i].n) continue;
+        for (int j = 0; j < ni; ++j)
+            if (ins[j].n && overlaps(outs[i].p, outs[i].n, ins[j].p, ins[j].n)) return false;
+        for (int j = i + 1; j < no; ++j)
+            if (outs[j].n && overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return false;
+    }
+    return true;
 }
 
 bool supported_head(int v) { return v == 16 || v == 32 || v == 64; }
@@ -368,31 +387,164 @@ int mate_compose_fwd(const void *y_ma, const void *y_te, const void *w_ma, const
 }
 
 
-int mate_gate_norm_fwd(const void *y, const void *z, const float *w, float eps, void *out,
-                       const mate_gate_norm_dims *d, void *stream)
+static int gate_norm_call(const void *y, const void *z, const float *w, float eps, void *out, int8_t *q, float *scale,
+                          const mate_gate_norm_dims *d, void *stream)
 {
     if (!d) return MATE_ERR_INVALID_ARG;
     if (d->tokens <= 0 || d->channels <= 0 || d->group <= 0 || !(eps >= 0.f) || !isfinite(eps))
         return MATE_ERR_INVALID_ARG;
     if (d->dtype != MATE_BF16) return MATE_ERR_UNSUPPORTED;
-    GateNormArgs a;
+    GateNormArgs a = {};
     a.M = d->tokens;
     a.C = d->channels;
     a.group = d->group;
     a.eps = eps;
     if (!gate_norm_supported(a)) return MATE_ERR_UNSUPPORTED;
-    if (!y || !z || !w || !out) return MATE_ERR_INVALID_ARG;
-    const void *ptrs[4] = {y, z, w, out};
+    if (!y || !z || !w || (q ? !scale : !out)) return MATE_ERR_INVALID_ARG;
+    const void *ptrs[5] = {y, z, w, out, q};
     for (const void *p : ptrs)
         if (!aligned(p, 16)) return MATE_ERR_INVALID_ARG;
     const size_t rb = (size_t)a.M * a.C * 2;
-    if (overlaps(out, rb, y, rb) || overlaps(out, rb, z, rb) || overlaps(out, rb, w, (size_t)a.C * 4))
-        return MATE_ERR_INVALID_ARG;
+    const Range ins[3] = {{y, rb}, {z, rb}, {w, (size_t)a.C * 4}};
+    if (q) {
+        if (!aligned(scale, 4)) return MATE_ERR_INVALID_ARG;
+        const Range outs[2] = {{q, rb / 2}, {scale, (size_t)a.M * 4}};
+        if (!disjoint(outs, 2, ins, 3)) return MATE_ERR_INVALID_ARG;
+    } else {
+        const Range outs[1] = {{out, rb}};
+        if (!disjoint(outs, 1, ins, 3)) return MATE_ERR_INVALID_ARG;
+    }
     a.y = y;
     a.z = z;
     a.w = w;
     a.out = out;
+    a.q = q;
+    a.scale = scale;
     return launch_gate_norm(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MATE_OK : MATE_ERR_CUDA;
+}
+
+int mate_gate_norm_fwd(const void *y, const void *z, const float *w, float eps, void *out,
+                       const mate_gate_norm_dims *d, void *stream)
+{
+    return gate_norm_call(y, z, w, eps, out, nullptr, nullptr, d, stream);
+}
+
+int mate_gate_norm_i8_fwd(const void *y, const void *z, const float *w, float eps, int8_t *q, float *scale,
+                          const mate_gate_norm_dims *d, void *stream)
+{
+    if (!q) return MATE_ERR_INVALID_ARG;
+    return gate_norm_call(y, z, w, eps, nullptr, q, scale, d, stream);
+}
+
+int mate_quant_rows_fwd(const void *x, int8_t *q, float *scale, const mate_quant_dims *d, void *stream)
+{
+    if (!d || d->rows <= 0 || d->k <= 0) return MATE_ERR_INVALID_ARG;
+    if (d->dtype != MATE_BF16) return MATE_ERR_UNSUPPORTED;
+    QuantArgs a = {};
+    a.M = d->rows;
+    a.K = d->k;
+    if (!quant_rows_supported(a)) return MATE_ERR_UNSUPPORTED;
+    if (!x || !q || !scale || !aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return MATE_ERR_INVALID_ARG;
+    const size_t nq = (size_t)a.M * a.K;
+    const Range outs[2] = {{q, nq}, {scale, (size_t)a.M * 4}}, ins[1] = {{x, nq * 2}};
+    if (!disjoint(outs, 2, ins, 1)) return MATE_ERR_INVALID_ARG;
+    a.x = x;
+    a.q = q;
+    a.scale = scale;
+    return launch_quant_rows(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MATE_OK : MATE_ERR_CUDA;
+}
+
+int mate_linear_i8_fwd(const int8_t *x, const float *x_scale, const int8_t *w, const float *w_scale,
+                       const float *bias, const void *addend, void *out, const mate_linear_i8_dims *d, void *stream)
+{
+    if (!d || d->tokens <= 0 || d->k <= 0 || d->n <= 0) return MATE_ERR_INVALID_ARG;
+    if (d->out_dtype != MATE_BF16 && d->out_dtype != MATE_F32) return MATE_ERR_UNSUPPORTED;
+    LinearI8Args a = {};
+    a.M = d->tokens;
+    a.N = d->n;
+    a.K = d->k;
+    a.out_f32 = d->out_dtype == MATE_F32;
+    if (!linear_i8_supported(a)) return MATE_ERR_UNSUPPORTED;
+    if (!x || !x_scale || !w || !w_scale || !out || !aligned(x_scale, 4)) return MATE_ERR_INVALID_ARG;
+    const void *ptrs[6] = {x, w, w_scale, bias, addend, out};
+    for (const void *p : ptrs)
+        if (!aligned(p, 16)) return MATE_ERR_INVALID_ARG;
+    const size_t ob = (size_t)a.M * a.N * (a.out_f32 ? 4 : 2);
+    const Range outs[1] = {{out, ob}};
+    const Range ins[6] = {{x, (size_t)a.M * a.K}, {x_scale, (size_t)a.M * 4}, {w, (size_t)a.N * a.K},
+                          {w_scale, (size_t)a.N * 4}, {bias, bias ? (size_t)a.N * 4 : 0},
+                          {addend, addend && addend != out ? ob : 0}};
+    if (!disjoint(outs, 1, ins, 6)) return MATE_ERR_INVALID_ARG;
+    a.x = x;
+    a.w = w;
+    a.x_scale = x_scale;
+    a.w_scale = w_scale;
+    a.bias = bias;
+    a.addend = addend;
+    a.out = out;
+    a.err = error_word_ptr();
+    if (!a.err) return MATE_ERR_CUDA;
+    return launch_linear_i8(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MATE_OK : MATE_ERR_CUDA;
+}
+
+int mate_block_norm_fwd(const void *x, const void *y, const float *w_post, const float *gate, const float *w_pre,
+                        const float *scale, const float *shift, void *x_out, void *h, float *h_scale,
+                        const mate_block_norm_dims *d, void *stream)
+{
+    if (!d || d->batch <= 0 || d->tokens <= 0 || d->channels <= 0 || !(d->eps >= 0.f) || !isfinite(d->eps) ||
+        !isfinite(d->residual_scale) || d->mod_stride < 0)
+        return MATE_ERR_INVALID_ARG;
+    if ((d->x_dtype != MATE_BF16 && d->x_dtype != MATE_F32) || d->post_norm < MATE_NORM_NONE ||
+        d->post_norm > MATE_NORM_LAYER)
+        return MATE_ERR_UNSUPPORTED;
+    // what the call does not use is not checked: the norm and type of an h that is not asked for
+    if (h && ((d->h_dtype != MATE_BF16 && d->h_dtype != MATE_I8) ||
+              (d->pre_norm != MATE_NORM_RMS && d->pre_norm != MATE_NORM_LAYER)))
+        return MATE_ERR_UNSUPPORTED;
+    BlockNormArgs a = {};
+    a.batch = d->batch;
+    a.n = d->tokens;
+    a.C = d->channels;
+    a.post = d->post_norm;
+    a.pre = d->pre_norm;
+    a.x_f32 = d->x_dtype == MATE_F32;
+    a.h_type = d->h_dtype;
+    a.mod_stride = d->mod_stride;
+    a.alpha = d->residual_scale;
+    a.eps = d->eps;
+    if (!block_norm_supported(a)) return MATE_ERR_UNSUPPORTED;
+    const bool i8 = h && a.h_type == MATE_I8;
+    if (!x || (!y && !h) || !y != !x_out || i8 != (h_scale != nullptr)) return MATE_ERR_INVALID_ARG;
+    if (!y && (w_post || gate)) return MATE_ERR_INVALID_ARG;
+    if (!h && (w_pre || scale || shift)) return MATE_ERR_INVALID_ARG;
+    const void *rows[4] = {x, y, x_out, h};
+    for (const void *p : rows)
+        if (!aligned(p, 16)) return MATE_ERR_INVALID_ARG;
+    const void *vecs[6] = {w_post, gate, w_pre, scale, shift, h_scale};
+    for (const void *p : vecs)
+        if (!aligned(p, 4)) return MATE_ERR_INVALID_ARG;
+    const size_t n = (size_t)a.batch * a.n * a.C, xb = n * (a.x_f32 ? 4 : 2), wb = (size_t)a.C * 4;
+    if ((uint64_t)a.mod_stride > ((uint64_t)1 << 40)) return MATE_ERR_UNSUPPORTED;
+    const size_t mb = ((size_t)(a.batch - 1) * (size_t)a.mod_stride + a.C) * 4;
+    const Range outs[3] = {{h, h ? n * (i8 ? 1 : 2) : 0},
+                           {h_scale, i8 ? (size_t)a.batch * a.n * 4 : 0},
+                           {x_out, x_out ? xb : 0}};
+    const Range ins[7] = {{y, y ? n * 2 : 0},       {w_post, w_post ? wb : 0}, {gate, gate ? mb : 0},
+                          {w_pre, w_pre ? wb : 0},  {scale, scale ? mb : 0},   {shift, shift ? mb : 0},
+                          {x, xb}};
+    // x_out may be x itself: each row is read whole before it is written
+    if (!disjoint(outs, 2, ins, 7) || !disjoint(outs, 3, ins, x_out == x ? 6 : 7)) return MATE_ERR_INVALID_ARG;
+    a.x = x;
+    a.y = y;
+    a.w_post = w_post;
+    a.gate = gate;
+    a.w_pre = w_pre;
+    a.scale = scale;
+    a.shift = shift;
+    a.x_out = x_out;
+    a.h = h;
+    a.h_scale = h_scale;
+    return launch_block_norm(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MATE_OK : MATE_ERR_CUDA;
 }
 
 size_t mate_frontend_workspace_bytes(int T, int H, int W, const mate_frontend_dims *d)
@@ -403,9 +555,11 @@ size_t mate_frontend_workspace_bytes(int T, int H, int W, const mate_frontend_di
     return total;
 }
 
-int mate_frontend_fwd(const void *u, const void *w_in, const float *conv_w, const float *conv_b, const float *dt_bias,
-                      int T, int H, int W, int scan_mode, void *z, void *x, float *dt, void *B, void *C,
-                      const mate_frontend_dims *d, void *workspace, size_t ws_bytes, void *stream)
+// u_scale and w_scale: u and w_in hold 8-bit codes (both null: bf16)
+static int frontend_call(const void *u, const float *u_scale, const void *w_in, const float *w_scale,
+                         const float *conv_w, const float *conv_b, const float *dt_bias, int T, int H, int W,
+                         int scan_mode, void *z, void *x, float *dt, void *B, void *C, const mate_frontend_dims *d,
+                         void *workspace, size_t ws_bytes, void *stream)
 {
     FrontArgs a;
     size_t pre = 0, total = 0;
@@ -419,23 +573,27 @@ int mate_frontend_fwd(const void *u, const void *w_in, const float *conv_w, cons
         return MATE_ERR_INVALID_ARG;
     if (!workspace || ws_bytes < total || !aligned(workspace, 256)) return MATE_ERR_WORKSPACE;
     const size_t M = (size_t)a.batch * a.N;
-    const size_t ub = M * a.d_model * 2, wb = (size_t)(a.d_inner + a.dc + a.nh) * a.d_model * 2;
+    const size_t e = u_scale ? 1 : 2, nr = (size_t)a.d_inner + a.dc + a.nh;
+    const size_t ub = M * a.d_model * e, wb = nr * a.d_model * e;
     const size_t zb = M * a.d_inner * 2, bb = M * a.G * a.Ns * 2, db = M * a.nh * 4;
     // every output disjoint from every input, from the workspace and from the other outputs
     const struct {
         const void *p;
         size_t n;
     } outs[5] = {{z, zb}, {x, zb}, {B, bb}, {C, bb}, {dt, db}},
-      ins[6] = {{u, ub}, {w_in, wb}, {conv_w, (size_t)a.dc * 16}, {conv_b, (size_t)a.dc * 4},
-                {dt_bias, (size_t)a.nh * 4}, {workspace, total}};
+      ins[8] = {{u, ub}, {w_in, wb}, {conv_w, (size_t)a.dc * 16}, {conv_b, (size_t)a.dc * 4},
+                {dt_bias, (size_t)a.nh * 4}, {workspace, total}, {u_scale, M * 4}, {w_scale, nr * 4}};
+    const int ni = u_scale ? 8 : 6;
     for (int i = 0; i < 5; ++i) {
-        for (int j = 0; j < 6; ++j)
+        for (int j = 0; j < ni; ++j)
             if (overlaps(outs[i].p, outs[i].n, ins[j].p, ins[j].n)) return MATE_ERR_INVALID_ARG;
         for (int j = i + 1; j < 5; ++j)
             if (overlaps(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return MATE_ERR_INVALID_ARG;
     }
     a.u = u;
     a.w_in = w_in;
+    a.u_scale = u_scale;
+    a.w_scale = w_scale;
     a.conv_w = conv_w;
     a.conv_b = conv_b;
     a.dt_bias = dt_bias;
@@ -449,6 +607,30 @@ int mate_frontend_fwd(const void *u, const void *w_in, const float *conv_w, cons
     a.err = error_word_ptr();
     if (!a.err) return MATE_ERR_CUDA;
     return launch_front(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? MATE_OK : MATE_ERR_CUDA;
+}
+
+int mate_frontend_fwd(const void *u, const void *w_in, const float *conv_w, const float *conv_b, const float *dt_bias,
+                      int T, int H, int W, int scan_mode, void *z, void *x, float *dt, void *B, void *C,
+                      const mate_frontend_dims *d, void *workspace, size_t ws_bytes, void *stream)
+{
+    return frontend_call(u, nullptr, w_in, nullptr, conv_w, conv_b, dt_bias, T, H, W, scan_mode, z, x, dt, B, C, d,
+                         workspace, ws_bytes, stream);
+}
+
+int mate_frontend_i8_fwd(const int8_t *u, const float *u_scale, const int8_t *w_in, const float *w_scale,
+                         const float *conv_w, const float *conv_b, const float *dt_bias, int T, int H, int W,
+                         int scan_mode, void *z, void *x, float *dt, void *B, void *C, const mate_frontend_dims *d,
+                         void *workspace, size_t ws_bytes, void *stream)
+{
+    FrontArgs a;
+    size_t pre = 0, total = 0;
+    const int rc = front_shape(T, H, W, scan_mode, d, a, pre, total);
+    if (rc != MATE_OK) return rc;
+    // the three products write rows of their own scales and outputs from 16-byte boundaries
+    if (a.d_inner % 8) return MATE_ERR_UNSUPPORTED;
+    if (!u_scale || !w_scale || !aligned(u_scale, 4) || !aligned(w_scale, 16)) return MATE_ERR_INVALID_ARG;
+    return frontend_call(u, u_scale, w_in, w_scale, conv_w, conv_b, dt_bias, T, H, W, scan_mode, z, x, dt, B, C, d,
+                         workspace, ws_bytes, stream);
 }
 
 int mate_debug_rms_map(int T, int H, int W, int scan_mode, int flip, int32_t *out_dev, void *stream)

@@ -47,6 +47,22 @@ bool tmap_bf16_5d(CUtensorMap *m, const void *base, const uint64_t dims[5], cons
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool tmap_2d(CUtensorMap *m, TmapType type, const void *base, uint64_t cols, uint64_t rows, uint32_t box_cols,
+             uint32_t box_rows)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const CUtensorMapDataType t = type == TmapType::u8     ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                  : type == TmapType::bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    const uint64_t e = type == TmapType::u8 ? 1 : type == TmapType::bf16 ? 2 : 4;
+    const cuuint64_t d[2] = {cols, rows}, st[1] = {cols * e};
+    const cuuint32_t bx[2] = {box_cols, box_rows}, es[2] = {1, 1};
+    return fn(m, t, 2, const_cast<void *>(base), d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 ScanBox scan_box(int mode, int T, int H, int W)
 {
     // axes fastest first, as the scan orders of rms_grid_offset walk them
