@@ -5,21 +5,26 @@
 // 127 * 127 * K below 2^31. The two scales, the bias and the addend are applied to it
 // in fp32 in the epilogue, and the result is rounded once to the output type.
 //
-// Persistent, one CTA per SM, 192 threads, in the manner of the bf16 composition GEMM
-// with rows of 128 codes in place of 64 bf16 values:
-//   warp 0    TMA loads of 128 x 128 x-tiles and 256 x 128 w-tiles into a 4-stage
-//             ring (48 KB per stage, 128-byte swizzle, K-major; codes past K, M or N
-//             load as zeros);
-//   warp 1    TMEM allocation and tcgen05.mma issue: per output tile of 128 x 256,
-//             four M = 128, N = 256, K = 32 MMAs per stage into one of two TMEM
-//             accumulators, so that a tile's epilogue runs while the next accumulates;
+// Persistent CTA pairs (clusters of two, cta_group::2), 192 threads per CTA; a pair
+// computes output tiles of 256 x 256, CTA r the rows 128 r ..:
+//   warp 0    TMA loads of the CTA's 128 x 128 codes of x and its half, 128 x 128, of
+//             the w tile into a 5-stage ring (32 KB per stage and CTA, 128-byte
+//             swizzle, K-major; codes past K, M or N load as zeros), all completing on
+//             the barriers of rank 0;
+//   warp 1    TMEM allocation and, in rank 0, tcgen05.mma issue: four M = 256, N = 256,
+//             K = 32 MMAs per stage into one of two TMEM accumulators (2 x 256 columns
+//             in each CTA), so that a tile's epilogue runs while the next accumulates;
 //   warps 2-5 the epilogue: TMEM -> registers -> scales, bias, addend -> a staging tile
-//             of 128 rows x 128 bytes in the 128-byte swizzle (two, alternating) -> TMA
-//             store.
+//             of 128 rows x 128 bytes in the 128-byte swizzle (four in turn) -> TMA
+//             store. The addend arrives in the staging tile by TMA, two tiles ahead.
+// A pair reads 64 KB for the work that two single CTAs would read 96 KB for: the pair
+// halves each CTA's share of w. Tiles go N fastest, so that the pairs at work share the
+// rows of x of a few tiles in L2, and all of w stays there.
 //
 // Every wait is bounded (2 s); a wait that gives up records MATE_ERR_TIMEOUT and
 // raises a CTA abort flag that makes every role leave its loop; the CTA then
-// waits (bounded) for its copies and MMAs in flight and frees its TMEM.
+// waits (bounded) for its copies and MMAs in flight, meets its peer (which leaves its
+// own waits by the same limit) and frees its TMEM.
 #include "common.cuh"
 #include "kernels.h"
 #include "tc.cuh"
@@ -31,18 +36,17 @@ namespace mate {
 
 namespace {
 
-constexpr int kBM = 128, kBN = 256, kBK = 128;  // a K step is 128 codes = one swizzled row
-constexpr int kStages = 4;
-constexpr uint32_t kATile = kBM * kBK;               // 16 KB
-constexpr uint32_t kBTile = kBN * kBK;               // 32 KB
-constexpr uint32_t kStage = kATile + kBTile;         // 48 KB
-constexpr uint32_t kOutTile = kBM * 128;             // 16 KB: 128 rows x 128 bytes
+constexpr int kBM = 256, kBN = 256, kBK = 128;       // tile of a pair; a K step is 128 codes = one swizzled row
+constexpr int kStages = 5, kSlots = 4;
+constexpr uint32_t kTile = 128 * kBK;                // 16 KB: one CTA's part of x or w
+constexpr uint32_t kStage = 2 * kTile;
+constexpr uint32_t kOutTile = 128 * 128;             // 16 KB: 128 rows x 128 bytes
 constexpr uint32_t kOffStages = 0;
-constexpr uint32_t kOffOut = kStages * kStage;       // 2 staging tiles
-constexpr uint32_t kOffBar = kOffOut + 2 * kOutTile;
-// full[4], empty[4], acc_full[2], acc_empty[2], drain; then the TMEM slot and the abort flag
+constexpr uint32_t kOffOut = kStages * kStage;
+constexpr uint32_t kOffBar = kOffOut + kSlots * kOutTile;
+// full, empty (per stage), acc_full[2], acc_empty[2], addend (per slot), drain; then the TMEM slot and the abort flag
 constexpr int kBarFull = 0, kBarEmpty = kStages, kBarAccFull = 2 * kStages, kBarAccEmpty = 2 * kStages + 2,
-              kBarDrain = 2 * kStages + 4, kNumBars = 2 * kStages + 5;
+              kBarAdd = 2 * kStages + 4, kBarDrain = kBarAdd + kSlots, kNumBars = kBarDrain + 1;
 constexpr uint32_t kOffMisc = kOffBar + 8 * kNumBars;
 constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;  // + alignment slack
 static_assert(kSmemBytes <= 227 * 1024, "linear_i8: shared memory");
@@ -54,12 +58,13 @@ struct Geo {
     int M, N, nk;        // rows, columns, 128-wide K steps
     int tiles_n, tiles;  // output tiles along N, in total
     const float *x_scale, *w_scale, *bias;
-    const void *addend;
+    int has_addend;
 };
 
-// eight (bf16) or four (fp32) outputs of one 16-byte chunk: columns n .. of row m
+// eight (bf16) or four (fp32) outputs, one 16-byte chunk of a staging tile: `acc` scaled, plus
+// the bias and the addend that `stg` holds
 template <bool F32>
-__device__ __forceinline__ uint4 finish(const uint32_t *acc, float xs, int m, int n, bool live, const Geo &geo)
+__device__ __forceinline__ uint4 finish(const uint32_t *acc, float xs, int n, const Geo &geo, const uint4 *stg)
 {
     constexpr int kCols = F32 ? 4 : 8;
     float v[kCols];
@@ -75,9 +80,8 @@ __device__ __forceinline__ uint4 finish(const uint32_t *acc, float xs, int m, in
             v[4 * q] += b.x, v[4 * q + 1] += b.y, v[4 * q + 2] += b.z, v[4 * q + 3] += b.w;
         }
     }
-    if (geo.addend && live) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const char *>(geo.addend) +
-                                                         ((int64_t)m * geo.N + n) * (F32 ? 4 : 2));
+    if (geo.has_addend) {
+        const uint4 u = *stg;
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -95,10 +99,21 @@ __device__ __forceinline__ uint4 finish(const uint32_t *acc, float xs, int m, in
                       tc::pack_bf16(v[6 % kCols], v[7 % kCols]));
 }
 
+// The staging tiles of a pair's CTA in the order it fills them: column chunks of its tiles.
+template <int OUT_COLS> struct Chunks {
+    int t, c;  // tile, column chunk
+    __device__ __forceinline__ void next(const Geo &geo, int step)
+    {
+        const int n0 = (t % geo.tiles_n) * kBN;
+        if (++c == kBN / OUT_COLS || n0 + OUT_COLS * c >= geo.N) c = 0, t += step;
+    }
+};
+
 template <bool F32>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_i8_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
-                     const __grid_constant__ CUtensorMap mo, const __grid_constant__ Geo geo, int *err)
+                     const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap md,
+                     const __grid_constant__ Geo geo, int *err)
 {
     constexpr int kOutCols = F32 ? 32 : 64;  // columns of a staging tile
     extern __shared__ uint8_t smem_raw[];
@@ -109,6 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(base + kOffMisc + 4);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = (int)tc::cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -117,15 +133,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&bars[kBarAccFull + i], 1);
-            tc::mbar_init(&bars[kBarAccEmpty + i], 128);
+            tc::mbar_init(&bars[kBarAccEmpty + i], 8);  // the epilogue warps of both CTAs
         }
+        for (int i = 0; i < kSlots; ++i) tc::mbar_init(&bars[kBarAdd + i], 1);
         tc::mbar_init(&bars[kBarDrain], 1);
         tc::fence_mbar_init();
         *abort_flag = 0;
     }
-    if (warp == 1) tc::tmem_alloc(tmem_slot, kTmemCols);
+    if (warp == 1) tc::tmem_alloc_pair(tmem_slot, kTmemCols);
     tc::tc_fence_before();
     __syncthreads();
+    tc::cluster_sync();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
@@ -133,31 +151,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- TMA producer ----------------
         if (lane == 0) {
             uint32_t it = 0;  // stage fills issued
-            for (int t = blockIdx.x; t < geo.tiles && !*abort_flag; t += gridDim.x) {
-                const int m0 = (t / geo.tiles_n) * kBM, n0 = (t % geo.tiles_n) * kBN;
+            for (int t = pair; t < geo.tiles && !*abort_flag; t += pairs) {
+                const int m0 = (t / geo.tiles_n) * kBM + rank * 128, n0 = (t % geo.tiles_n) * kBN + rank * 128;
                 for (int ks = 0; ks < geo.nk; ++ks, ++it) {
                     const int s = it % kStages;
                     const uint32_t round = it / kStages;
                     if (round > 0 && !tc::mbar_wait_or_abort(&bars[kBarEmpty + s], (round - 1) & 1u, err, abort_flag))
                         break;
-                    uint8_t *sa = base + kOffStages + s * kStage, *sb = sa + kATile;
-                    tc::mbar_expect_tx(&bars[kBarFull + s], kStage);
-                    tc::tma_load_2d(sa, &ma, &bars[kBarFull + s], ks * kBK, m0);
-                    tc::tma_load_2d(sb, &mb, &bars[kBarFull + s], ks * kBK, n0);
+                    uint8_t *sa = base + kOffStages + s * kStage, *sb = sa + kTile;
+                    // both CTAs' four copies complete on rank 0's barrier
+                    const uint32_t full = tc::cluster_addr(&bars[kBarFull + s], 0);
+                    if (rank == 0) tc::mbar_expect_tx(&bars[kBarFull + s], 2 * kStage);
+                    tc::tma_load_2d_pair(sa, &ma, full, ks * kBK, m0);
+                    tc::tma_load_2d_pair(sb, &mb, full, ks * kBK, n0);
                 }
             }
-            // every load issued has landed before the CTA may leave (bounded)
-            if (it > 0) {
+            // every load issued has landed before the CTA may leave (bounded; rank 0 sees both CTAs')
+            if (rank == 0 && it > 0) {
                 const uint32_t last = it - 1;
                 tc::mbar_wait(&bars[kBarFull + last % kStages], (last / kStages) & 1u, nullptr);
             }
         }
     } else if (warp == 1) {
         // ---------------- MMA issue ----------------
-        if (lane == 0) {
+        if (lane == 0 && rank == 0) {
             const uint32_t idesc = tc::idesc_i8(kBM, kBN);
             uint32_t it = 0, tl = 0, committed = 0;
-            for (int t = blockIdx.x; t < geo.tiles && !*abort_flag; t += gridDim.x, ++tl) {
+            for (int t = pair; t < geo.tiles && !*abort_flag; t += pairs, ++tl) {
                 const uint32_t acc = tl & 1, use = tl >> 1;
                 if (use > 0 && !tc::mbar_wait_or_abort(&bars[kBarAccEmpty + acc], (use - 1) & 1u, err, abort_flag))
                     break;
@@ -171,20 +191,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     tc::tc_fence_after();
-                    const uint32_t a0 = tc::smem_u32(base + kOffStages + s * kStage), b0 = a0 + kATile;
+                    const uint32_t a0 = tc::smem_u32(base + kOffStages + s * kStage), b0 = a0 + kTile;
 #pragma unroll
                     for (int kk = 0; kk < kBK / 32; ++kk)
-                        tc::mma_i8(d, tc::sdesc_sw128(a0 + kk * 32, 16, 1024), tc::sdesc_sw128(b0 + kk * 32, 16, 1024),
-                                   idesc, ks > 0 || kk > 0);
-                    tc::mma_commit(&bars[kBarEmpty + s]);  // the stage is free once these MMAs are done
+                        tc::mma_i8_pair(d, tc::sdesc_sw128(a0 + kk * 32, 16, 1024),
+                                        tc::sdesc_sw128(b0 + kk * 32, 16, 1024), idesc, ks > 0 || kk > 0);
+                    tc::mma_commit_pair(&bars[kBarEmpty + s]);  // the stage is free in both CTAs once these MMAs are done
                     ++committed;
                 }
                 if (!ok) break;
-                tc::mma_commit(&bars[kBarAccFull + acc]);
+                tc::mma_commit_pair(&bars[kBarAccFull + acc]);
             }
             // every MMA issued has completed before TMEM may be freed (bounded)
             if (committed > 0) {
-                tc::mma_commit(&bars[kBarDrain]);
+                tc::mma_commit_pair(&bars[kBarDrain]);
                 tc::mbar_wait(&bars[kBarDrain], 0, nullptr);
             }
         }
@@ -192,53 +212,84 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- epilogue: warps 2-5, TMEM lanes 32 (warp % 4) .. ----------------
         const int et = tid - 64;                        // 0..127
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32);
-        const int row = (int)lane_base + lane;          // output row of the tile
-        uint32_t tl = 0, chunks = 0;                    // tiles and staging tiles stored
-        for (int t = blockIdx.x; t < geo.tiles; t += gridDim.x, ++tl) {
+        const int row = (int)lane_base + lane;          // output row of the CTA's half tile
+        uint32_t tl = 0, chunks = 0;                    // tiles and staging tiles done
+        Chunks<kOutCols> ahead{pair, 0};                // the next addend chunk to ask for
+        uint32_t asked = 0;
+        auto ask = [&] {  // one thread: the addend of the next chunk into its slot
+            if (ahead.t >= geo.tiles) return;
+            const uint32_t slot = asked % kSlots;
+            tc::mbar_expect_tx(&bars[kBarAdd + slot], kOutTile);
+            tc::tma_load_2d(base + kOffOut + slot * kOutTile, &md, &bars[kBarAdd + slot],
+                            (ahead.t % geo.tiles_n) * kBN + kOutCols * ahead.c,
+                            (ahead.t / geo.tiles_n) * kBM + rank * 128);
+            ++asked;
+            ahead.next(geo, pairs);
+        };
+        if (geo.has_addend && et == 0) ask(), ask();
+        bool ok = true;
+        for (int t = pair; t < geo.tiles && ok; t += pairs, ++tl) {
             const uint32_t acc = tl & 1, use = tl >> 1;
-            if (!tc::mbar_wait_sleep(&bars[kBarAccFull + acc], use & 1u, err, abort_flag)) break;
+            if (!tc::named_all(1, 128, tc::mbar_wait_sleep(&bars[kBarAccFull + acc], use & 1u, err, abort_flag))) break;
             tc::tc_fence_after();
-            const int m0 = (t / geo.tiles_n) * kBM, n0 = (t % geo.tiles_n) * kBN;
-            const bool live = m0 + row < geo.M;
-            const float xs = live ? geo.x_scale[m0 + row] : 0.f;
+            const int m0 = (t / geo.tiles_n) * kBM + rank * 128, n0 = (t % geo.tiles_n) * kBN;
+            const float xs = m0 + row < geo.M ? geo.x_scale[m0 + row] : 0.f;
             for (int c = 0; c < kBN / kOutCols && n0 + kOutCols * c < geo.N; ++c, ++chunks) {
+                const uint32_t slot = chunks % kSlots;
                 uint32_t v[kOutCols / 32][32];
 #pragma unroll
                 for (int q = 0; q < kOutCols / 32; ++q)
                     tc::tmem_ld32u(tc::tmem_addr(tmem + acc * kBN, lane_base, kOutCols * c + 32 * q), v[q]);
                 tc::tmem_wait_ld();
-                // the store that read this staging tile two chunks ago is done with it
-                if (et == 0) tc::bulk_wait_read<1>();
-                tc::named_sync(1, 128);
-                uint8_t *stg = base + kOffOut + (chunks & 1) * kOutTile;
+                if (geo.has_addend) {
+                    // asked for after the store that read this slot was done with it
+                    ok = tc::named_all(1, 128, tc::mbar_wait_or_abort(&bars[kBarAdd + slot], (chunks / kSlots) & 1u, err,
+                                                                      abort_flag));
+                    if (!ok) break;
+                } else {
+                    if (et == 0) tc::bulk_wait_read<kSlots - 1>();
+                    tc::named_sync(1, 128);
+                }
+                uint8_t *stg = base + kOffOut + slot * kOutTile;
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     const int n = n0 + kOutCols * c + q * (kOutCols / 8);
+                    uint4 *at = reinterpret_cast<uint4 *>(stg + tc::sw128(row, q));
                     // N is a multiple of 8: a 16-byte chunk is inside or outside as a whole
                     if (n < geo.N)
-                        *reinterpret_cast<uint4 *>(stg + tc::sw128(row, q)) =
-                            finish<F32>(&v[q * (kOutCols / 8) / 32][q * (kOutCols / 8) % 32], xs, m0 + row, n, live, geo);
+                        *at = finish<F32>(&v[q * (kOutCols / 8) / 32][q * (kOutCols / 8) % 32], xs, n, geo, at);
                 }
                 tc::fence_proxy_async_smem();
                 tc::named_sync(1, 128);
                 if (et == 0) {
                     // rows past M and columns past N fall outside the tensor and are not written
-                    tc::tma_store_2d(&mo, stg, n0 + kOutCols * c, m0);
+                    if (m0 < geo.M) tc::tma_store_2d(&mo, stg, n0 + kOutCols * c, m0);
                     tc::bulk_commit();
+                    if (geo.has_addend) {
+                        tc::bulk_wait_read<kSlots - 2>();  // the slot two chunks on is free again
+                        ask();
+                    }
                 }
             }
             // this accumulator may be overwritten by the tile after next
             tc::tc_fence_before();
-            tc::mbar_arrive(&bars[kBarAccEmpty + acc]);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(tc::cluster_addr(&bars[kBarAccEmpty + acc], 0));
         }
-        if (et == 0) tc::bulk_wait_all();
+        if (et == 0) {
+            // the addends asked for have landed (bounded), the stores have completed
+            for (uint32_t i = chunks; i < asked; ++i)
+                tc::mbar_wait(&bars[kBarAdd + i % kSlots], (i / kSlots) & 1u, nullptr);
+            tc::bulk_wait_all();
+        }
     }
 
     tc::tc_fence_before();
     __syncthreads();
+    tc::cluster_sync();  // the peer's loads, commits and arrivals reach this CTA's shared memory until here
     if (warp == 1) {
         tc::tc_fence_after();
-        tc::tmem_dealloc(tmem, kTmemCols);
+        tc::tmem_dealloc_pair(tmem, kTmemCols);
     }
 }
 
@@ -258,9 +309,11 @@ cudaError_t launch_linear_i8(const LinearI8Args &a, cudaStream_t s)
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e != cudaSuccess) return e;
     if (!tmap_available()) return cudaErrorNotSupported;
-    CUtensorMap ma, mb, mo;
-    if (!tmap_2d(&ma, TmapType::u8, a.x, a.K, a.M, kBK, kBM) || !tmap_2d(&mb, TmapType::u8, a.w, a.K, a.N, kBK, kBN) ||
-        !tmap_2d(&mo, a.out_f32 ? TmapType::f32 : TmapType::bf16, a.out, a.N, a.M, a.out_f32 ? 32 : 64, kBM))
+    const TmapType ot = a.out_f32 ? TmapType::f32 : TmapType::bf16;
+    const int oc = a.out_f32 ? 32 : 64;
+    CUtensorMap ma, mb, mo, md;
+    if (!tmap_2d(&ma, TmapType::u8, a.x, a.K, a.M, kBK, 128) || !tmap_2d(&mb, TmapType::u8, a.w, a.K, a.N, kBK, 128) ||
+        !tmap_2d(&mo, ot, a.out, a.N, a.M, oc, 128) || !tmap_2d(&md, ot, a.addend ? a.addend : a.out, a.N, a.M, oc, 128))
         return cudaErrorInvalidValue;
     Geo geo;
     geo.M = a.M;
@@ -271,12 +324,12 @@ cudaError_t launch_linear_i8(const LinearI8Args &a, cudaStream_t s)
     geo.x_scale = a.x_scale;
     geo.w_scale = a.w_scale;
     geo.bias = a.bias;
-    geo.addend = a.addend;
+    geo.has_addend = a.addend != nullptr;
     int dev = 0, nsm = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
-    const int grid = std::min(geo.tiles, std::max(nsm, 1));
+    const int grid = 2 * std::min(geo.tiles, std::max(nsm / 2, 1));
     Phase ph(a.phase ? a.phase : MATE_PHASE_LINEAR_I8, s);
-    kernel<<<grid, kThreads, kSmemBytes, s>>>(ma, mb, mo, geo, a.err);
+    kernel<<<grid, kThreads, kSmemBytes, s>>>(ma, mb, mo, md, geo, a.err);
     return cudaGetLastError();
 }
 
