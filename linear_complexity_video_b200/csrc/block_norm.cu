@@ -109,32 +109,40 @@ __global__ void __launch_bounds__(kBnThreads, 2) block_norm_kernel(BlockNormArgs
     RowReduce<TPR> red{part, slot};
     const float inv_c = 1.f / (float)a.C;
 
-    for (int i = r0 + slot; i < r1; i += kRows) {
-        const int64_t row = (int64_t)b * a.n + i, at = row * a.C;
-        float r[VPL][8];
-        uint4 yv[VPL];
+    uint4 yv[VPL], xv[XF32 ? 2 * VPL : VPL];
+    auto load = [&](int i) {
+        const int64_t at = ((int64_t)b * a.n + i) * a.C;
+        const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const char *>(a.x) + at * (XF32 ? 4 : 2));
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            const int v = t + j * TPR;
+            if (XF32) {
+                xv[2 * j] = v < nv ? __ldcs(x + 2 * v) : make_uint4(0, 0, 0, 0);
+                xv[XF32 ? 2 * j + 1 : 0] = v < nv ? __ldcs(x + 2 * v + 1) : make_uint4(0, 0, 0, 0);
+            } else {
+                xv[j] = v < nv ? __ldcs(x + v) : make_uint4(0, 0, 0, 0);
+            }
+        }
         if (a.y) {
             const uint4 *y = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.y) + at);
 #pragma unroll
             for (int j = 0; j < VPL; ++j) yv[j] = t + j * TPR < nv ? __ldcs(y + t + j * TPR) : make_uint4(0, 0, 0, 0);
         }
-        uint4 xv[XF32 ? 1 : VPL];
+    };
+    auto unpack_x = [&](int j, float (&f)[8]) {
         if (XF32) {
-            const float4 *x = reinterpret_cast<const float4 *>(static_cast<const float *>(a.x) + at);
-#pragma unroll
-            for (int j = 0; j < VPL; ++j) {
-                const int v = t + j * TPR;
-                const float4 p = v < nv ? __ldcs(x + 2 * v) : make_float4(0, 0, 0, 0);
-                const float4 q = v < nv ? __ldcs(x + 2 * v + 1) : make_float4(0, 0, 0, 0);
-                r[j][0] = p.x, r[j][1] = p.y, r[j][2] = p.z, r[j][3] = p.w;
-                r[j][4] = q.x, r[j][5] = q.y, r[j][6] = q.z, r[j][7] = q.w;
-            }
+            const uint4 p = xv[2 * j], q = xv[XF32 ? 2 * j + 1 : 0];
+            f[0] = __uint_as_float(p.x), f[1] = __uint_as_float(p.y), f[2] = __uint_as_float(p.z);
+            f[3] = __uint_as_float(p.w), f[4] = __uint_as_float(q.x), f[5] = __uint_as_float(q.y);
+            f[6] = __uint_as_float(q.z), f[7] = __uint_as_float(q.w);
         } else {
-            const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.x) + at);
-#pragma unroll
-            for (int j = 0; j < VPL; ++j)
-                xv[XF32 ? 0 : j] = t + j * TPR < nv ? __ldcs(x + t + j * TPR) : make_uint4(0, 0, 0, 0);
+            unpack8(xv[j], f);
         }
+    };
+    if (r0 + slot < r1) load(r0 + slot);
+    for (int i = r0 + slot; i < r1; i += kRows) {
+        const int64_t row = (int64_t)b * a.n + i, at = row * a.C;
+        float r[VPL][8];
         if (a.y) {
             float mu = 0.f, rs = 1.f;
             if (a.post == MATE_NORM_LAYER) {
@@ -168,7 +176,7 @@ __global__ void __launch_bounds__(kBnThreads, 2) block_norm_kernel(BlockNormArgs
                     float f[8], g[8];
                     unpack8(yv[j], f);
                     load8(cg, nv, v, g);
-                    if (!XF32) unpack8(xv[XF32 ? 0 : j], r[j]);
+                    unpack_x(j, r[j]);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) r[j][e] = fmaf((f[e] - mu) * rs, g[e], a.alpha * r[j][e]);
                     if (XF32) {
@@ -185,10 +193,12 @@ __global__ void __launch_bounds__(kBnThreads, 2) block_norm_kernel(BlockNormArgs
                     for (int e = 0; e < 8; ++e) r[j][e] = 0.f;
                 }
             }
-        } else if (!XF32) {
+        } else {
 #pragma unroll
-            for (int j = 0; j < VPL; ++j) unpack8(xv[XF32 ? 0 : j], r[j]);
+            for (int j = 0; j < VPL; ++j) unpack_x(j, r[j]);
         }
+        // the packed row is used up: the next one's loads run under the rest of this one
+        if (i + kRows < r1) load(i + kRows);
         if (!a.h) continue;
         float mu = 0.f;
         if (a.pre == MATE_NORM_LAYER) {
@@ -265,9 +275,10 @@ template <int TPR, int VPL, bool XF32> cudaError_t launch(const BlockNormArgs &a
 template <bool XF32> cudaError_t dispatch(const BlockNormArgs &a, cudaStream_t s)
 {
     const int nv = a.C / 8;
-    if (nv <= 32 * 5) return launch<32, 5, XF32>(a, s);
-    if (nv <= 64 * 5) return launch<64, 5, XF32>(a, s);
-    if (nv <= 128 * 5) return launch<128, 5, XF32>(a, s);
+    constexpr int kV = XF32 ? 3 : 5;  // fp32 rows take twice the registers
+    if (nv <= 32 * kV) return launch<32, kV, XF32>(a, s);
+    if (nv <= 64 * kV) return launch<64, kV, XF32>(a, s);
+    if (nv <= 128 * kV) return launch<128, kV, XF32>(a, s);
     return launch<256, 4, XF32>(a, s);
 }
 

@@ -20,6 +20,8 @@
 
 #include <cuda_bf16.h>
 
+#include <algorithm>
+
 namespace mate {
 
 namespace {
@@ -31,11 +33,8 @@ constexpr int kGnMaxVec = 8;  // vectors per thread: rows of up to 8 x 8 x 128 =
 // far below the bf16 rounding of the result, for either sign of v)
 __device__ __forceinline__ float silu_fast(float v) { return __fdividef(v, 1.f + __expf(-v)); }
 
-// I8: the output row as 8-bit codes and a scale (i8.cuh) instead of bf16: one more
-// pass over the registers for the row's largest magnitude
-template <bool I8> __global__ void __launch_bounds__(kGnThreads) gate_norm_kernel(GateNormArgs a)
+__global__ void __launch_bounds__(kGnThreads) gate_norm_kernel(GateNormArgs a)
 {
-    __shared__ uint32_t amax[kGnThreads / 32];
     __shared__ float ss_vec[kGnMaxVec * kGnThreads];  // sum of squares of each vector of the row
     __shared__ float scale[kGnMaxVec * kGnThreads];   // 1 / rms of each group (at most one per vector)
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -81,7 +80,6 @@ template <bool I8> __global__ void __launch_bounds__(kGnThreads) gate_norm_kerne
     }
     __syncthreads();
     uint4 *out = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + row);
-    float m = 0.f;
     const float4 *w4 = reinterpret_cast<const float4 *>(a.w);
 #pragma unroll
     for (int j = 0; j < kGnMaxVec; ++j) {
@@ -90,31 +88,89 @@ template <bool I8> __global__ void __launch_bounds__(kGnThreads) gate_norm_kerne
             const float f = scale[v / gv];
             const float4 wa = w4[2 * v], wb = w4[2 * v + 1];
             const float wv[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
-            if constexpr (I8) {
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                o[e] = tc::pack_bf16(g[j][2 * e] * f * wv[2 * e], g[j][2 * e + 1] * f * wv[2 * e + 1]);
+            out[v] = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+}
+
+// The same values as 8-bit codes and one scale per row (i8.cuh). The row's largest magnitude
+// is a second reduction between the loads and the stores of a row, so a CTA keeps the next
+// row's loads in flight meanwhile: persistent CTAs, and the packed vectors of a row are used
+// up before its sums are.
+template <int VPL> __global__ void __launch_bounds__(kGnThreads) gate_norm_i8_kernel(GateNormArgs a)
+{
+    __shared__ float ss_vec[VPL * kGnThreads];
+    __shared__ float scale[VPL * kGnThreads];
+    __shared__ uint32_t amax[kGnThreads / 32];
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const int nv = a.C / 8, gv = a.group / 8, ng = a.C / a.group;
+    uint4 yv[VPL], zv[VPL];
+    auto load = [&](int64_t r) {
+        const uint4 *y = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.y) + r * a.C);
+        const uint4 *z = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.z) + r * a.C);
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            const int v = t + j * kGnThreads;
+            yv[j] = v < nv ? __ldcs(y + v) : make_uint4(0, 0, 0, 0);
+            zv[j] = v < nv ? __ldcs(z + v) : make_uint4(0, 0, 0, 0);
+        }
+    };
+    load(blockIdx.x);
+    for (int64_t r = blockIdx.x; r < a.M; r += gridDim.x) {
+        float g[VPL][8];
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            const uint32_t yw[4] = {yv[j].x, yv[j].y, yv[j].z, yv[j].w};
+            const uint32_t zw[4] = {zv[j].x, zv[j].y, zv[j].z, zv[j].w};
+            float s = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 yf = tc::unpack_bf16(yw[e]), zf = tc::unpack_bf16(zw[e]);
+                g[j][2 * e] = yf.x * silu_fast(zf.x);
+                g[j][2 * e + 1] = yf.y * silu_fast(zf.y);
+                s = fmaf(g[j][2 * e], g[j][2 * e], s);
+                s = fmaf(g[j][2 * e + 1], g[j][2 * e + 1], s);
+            }
+            if (t + j * kGnThreads < nv) ss_vec[t + j * kGnThreads] = s;
+        }
+        if (r + gridDim.x < a.M) load(r + gridDim.x);
+        __syncthreads();
+        for (int gi = warp; gi < ng; gi += kGnThreads / 32) {
+            float s = 0.f;
+            for (int v = gi * gv + lane; v < (gi + 1) * gv; v += 32) s += ss_vec[v];
+            s = warp_sum(s);
+            if (lane == 0) scale[gi] = rsqrtf(s / (float)a.group + a.eps);
+        }
+        __syncthreads();
+        const float4 *w4 = reinterpret_cast<const float4 *>(a.w);
+        float m = 0.f;
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+            const int v = t + j * kGnThreads;
+            if (v < nv) {
+                const float f = scale[v / gv];
+                const float4 wa = w4[2 * v], wb = w4[2 * v + 1];
+                const float wv[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     g[j][e] = g[j][e] * f * wv[e];
                     m = i8::amax_nan(m, g[j][e]);
                 }
-            } else {
-                uint32_t o[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    o[e] = tc::pack_bf16(g[j][2 * e] * f * wv[2 * e], g[j][2 * e + 1] * f * wv[2 * e + 1]);
-                out[v] = make_uint4(o[0], o[1], o[2], o[3]);
             }
         }
-    }
-    if constexpr (I8) {
         uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
         if (lane == 0) amax[warp] = mb;
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kGnThreads / 32; ++i) mb = max(mb, amax[i]);
         const i8::RowScale rs = i8::row_scale(__uint_as_float(mb));
-        uint2 *q = reinterpret_cast<uint2 *>(a.q + row);
+        uint2 *q = reinterpret_cast<uint2 *>(a.q + r * a.C);
 #pragma unroll
-        for (int j = 0; j < kGnMaxVec; ++j) {
+        for (int j = 0; j < VPL; ++j) {
             const int v = t + j * kGnThreads;
             if (v < nv) {
                 if (rs.pre != 1.f) {  // zero, tiny or not finite (where 0 * v would be NaN)
@@ -125,8 +181,17 @@ template <bool I8> __global__ void __launch_bounds__(kGnThreads) gate_norm_kerne
                                   i8::codes4(g[j][4], g[j][5], g[j][6], g[j][7], rs.mul));
             }
         }
-        if (t == 0) a.scale[blockIdx.x] = rs.scale;
+        if (t == 0) a.scale[r] = rs.scale;
     }
+}
+
+template <int VPL> cudaError_t launch_i8(const GateNormArgs &a, cudaStream_t s)
+{
+    int dev = 0, nsm = 148, per_sm = 4;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, gate_norm_i8_kernel<VPL>, kGnThreads, 0);
+    gate_norm_i8_kernel<VPL><<<std::min(a.M, std::max(1, nsm * per_sm)), kGnThreads, 0, s>>>(a);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -140,10 +205,11 @@ bool gate_norm_supported(const GateNormArgs &a)
 cudaError_t launch_gate_norm(const GateNormArgs &a, cudaStream_t s)
 {
     Phase ph(MATE_PHASE_GATE_NORM, s);
-    if (a.q)
-        gate_norm_kernel<true><<<a.M, kGnThreads, 0, s>>>(a);
-    else
-        gate_norm_kernel<false><<<a.M, kGnThreads, 0, s>>>(a);
+    if (a.q) {
+        const int nv = a.C / 8;
+        return nv <= 2 * kGnThreads ? launch_i8<2>(a, s) : nv <= 5 * kGnThreads ? launch_i8<5>(a, s) : launch_i8<kGnMaxVec>(a, s);
+    }
+    gate_norm_kernel<<<a.M, kGnThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 

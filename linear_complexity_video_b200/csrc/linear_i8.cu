@@ -15,11 +15,12 @@
 //             K = 32 MMAs per stage into one of two TMEM accumulators (2 x 256 columns
 //             in each CTA), so that a tile's epilogue runs while the next accumulates;
 //   warps 2-5 the epilogue: TMEM -> registers -> scales, bias, addend -> a staging tile
-//             of 128 rows x 128 bytes in the 128-byte swizzle (four in turn) -> TMA
-//             store. The addend arrives in the staging tile by TMA, two tiles ahead.
+//             of 128 rows x 128 bytes in the 128-byte swizzle (three in turn) -> TMA
+//             store. The addend arrives in the staging tile by TMA, two tiles ahead; the
+//             columns' scales and bias wait in shared memory, fetched a tile ahead.
 // A pair reads 64 KB for the work that two single CTAs would read 96 KB for: the pair
-// halves each CTA's share of w. Tiles go N fastest, so that the pairs at work share the
-// rows of x of a few tiles in L2, and all of w stays there.
+// halves each CTA's share of w. Tiles are walked in groups of eight tile rows, so that the
+// 74 pairs at work read about eight rows' x and nine columns' w.
 //
 // Every wait is bounded (2 s); a wait that gives up records MATE_ERR_TIMEOUT and
 // raises a CTA abort flag that makes every role leave its loop; the CTA then
@@ -37,13 +38,15 @@ namespace mate {
 namespace {
 
 constexpr int kBM = 256, kBN = 256, kBK = 128;       // tile of a pair; a K step is 128 codes = one swizzled row
-constexpr int kStages = 5, kSlots = 4;
+constexpr int kStages = 5, kSlots = 3;
+constexpr int kGroup = 8;                            // tile rows walked together
 constexpr uint32_t kTile = 128 * kBK;                // 16 KB: one CTA's part of x or w
 constexpr uint32_t kStage = 2 * kTile;
 constexpr uint32_t kOutTile = 128 * 128;             // 16 KB: 128 rows x 128 bytes
 constexpr uint32_t kOffStages = 0;
 constexpr uint32_t kOffOut = kStages * kStage;
-constexpr uint32_t kOffBar = kOffOut + kSlots * kOutTile;
+constexpr uint32_t kOffVec = kOffOut + kSlots * kOutTile;  // w_scale and bias of the tile's columns
+constexpr uint32_t kOffBar = kOffVec + 2 * kBN * 4;
 // full, empty (per stage), acc_full[2], acc_empty[2], addend (per slot), drain; then the TMEM slot and the abort flag
 constexpr int kBarFull = 0, kBarEmpty = kStages, kBarAccFull = 2 * kStages, kBarAccEmpty = 2 * kStages + 2,
               kBarAdd = 2 * kStages + 4, kBarDrain = kBarAdd + kSlots, kNumBars = kBarDrain + 1;
@@ -56,27 +59,39 @@ constexpr int kMaxK = 131072;
 
 struct Geo {
     int M, N, nk;        // rows, columns, 128-wide K steps
-    int tiles_n, tiles;  // output tiles along N, in total
+    int tiles_m, tiles_n, tiles;  // output tiles along M, along N, in total
     const float *x_scale, *w_scale, *bias;
     int has_addend;
 };
 
+// Tile t of the walk: groups of kGroup tile rows, columns in turn inside a group, the
+// group's rows fastest.
+struct Tile {
+    int m, n;
+};
+__device__ __forceinline__ Tile tile_at(int t, const Geo &geo)
+{
+    const int g = t / (kGroup * geo.tiles_n), r = t - g * kGroup * geo.tiles_n;
+    const int rows = min(kGroup, geo.tiles_m - g * kGroup);
+    return {(g * kGroup + r % rows) * kBM, (r / rows) * kBN};
+}
+
 // eight (bf16) or four (fp32) outputs, one 16-byte chunk of a staging tile: `acc` scaled, plus
-// the bias and the addend that `stg` holds
+// the bias (`vec`: the columns' w_scale, their bias kBN floats on) and the addend that `stg` holds
 template <bool F32>
-__device__ __forceinline__ uint4 finish(const uint32_t *acc, float xs, int n, const Geo &geo, const uint4 *stg)
+__device__ __forceinline__ uint4 finish(const uint32_t *acc, float xs, const float *vec, const Geo &geo, const uint4 *stg)
 {
     constexpr int kCols = F32 ? 4 : 8;
     float v[kCols];
 #pragma unroll
     for (int q = 0; q < kCols / 4; ++q) {
-        const float4 ws = *reinterpret_cast<const float4 *>(geo.w_scale + n + 4 * q);
+        const float4 ws = *reinterpret_cast<const float4 *>(vec + 4 * q);
         v[4 * q] = (float)(int)acc[4 * q] * xs * ws.x;
         v[4 * q + 1] = (float)(int)acc[4 * q + 1] * xs * ws.y;
         v[4 * q + 2] = (float)(int)acc[4 * q + 2] * xs * ws.z;
         v[4 * q + 3] = (float)(int)acc[4 * q + 3] * xs * ws.w;
         if (geo.bias) {
-            const float4 b = *reinterpret_cast<const float4 *>(geo.bias + n + 4 * q);
+            const float4 b = *reinterpret_cast<const float4 *>(vec + kBN + 4 * q);
             v[4 * q] += b.x, v[4 * q + 1] += b.y, v[4 * q + 2] += b.z, v[4 * q + 3] += b.w;
         }
     }
@@ -104,7 +119,7 @@ template <int OUT_COLS> struct Chunks {
     int t, c;  // tile, column chunk
     __device__ __forceinline__ void next(const Geo &geo, int step)
     {
-        const int n0 = (t % geo.tiles_n) * kBN;
+        const int n0 = tile_at(t, geo).n;
         if (++c == kBN / OUT_COLS || n0 + OUT_COLS * c >= geo.N) c = 0, t += step;
     }
 };
@@ -152,7 +167,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             uint32_t it = 0;  // stage fills issued
             for (int t = pair; t < geo.tiles && !*abort_flag; t += pairs) {
-                const int m0 = (t / geo.tiles_n) * kBM + rank * 128, n0 = (t % geo.tiles_n) * kBN + rank * 128;
+                const Tile at = tile_at(t, geo);
+                const int m0 = at.m + rank * 128, n0 = at.n + rank * 128;
                 for (int ks = 0; ks < geo.nk; ++ks, ++it) {
                     const int s = it % kStages;
                     const uint32_t round = it / kStages;
@@ -220,19 +236,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (ahead.t >= geo.tiles) return;
             const uint32_t slot = asked % kSlots;
             tc::mbar_expect_tx(&bars[kBarAdd + slot], kOutTile);
-            tc::tma_load_2d(base + kOffOut + slot * kOutTile, &md, &bars[kBarAdd + slot],
-                            (ahead.t % geo.tiles_n) * kBN + kOutCols * ahead.c,
-                            (ahead.t / geo.tiles_n) * kBM + rank * 128);
+            const Tile at = tile_at(ahead.t, geo);
+            tc::tma_load_2d(base + kOffOut + slot * kOutTile, &md, &bars[kBarAdd + slot], at.n + kOutCols * ahead.c,
+                            at.m + rank * 128);
             ++asked;
             ahead.next(geo, pairs);
         };
         if (geo.has_addend && et == 0) ask(), ask();
+        // the scales and biases of a tile's columns et and et + 128
+        float *vec = reinterpret_cast<float *>(base + kOffVec);
+        float ws[2], bs[2];
+        auto fetch = [&](int t) {
+            const int n = t < geo.tiles ? tile_at(t, geo).n + et : geo.N;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                ws[h] = n + 128 * h < geo.N ? geo.w_scale[n + 128 * h] : 0.f;
+                bs[h] = geo.bias && n + 128 * h < geo.N ? geo.bias[n + 128 * h] : 0.f;
+            }
+        };
+        fetch(pair);
         bool ok = true;
         for (int t = pair; t < geo.tiles && ok; t += pairs, ++tl) {
             const uint32_t acc = tl & 1, use = tl >> 1;
+            // the last tile's readers passed the barrier of its last chunk
+#pragma unroll
+            for (int h = 0; h < 2; ++h) vec[et + 128 * h] = ws[h], vec[kBN + et + 128 * h] = bs[h];
+            fetch(t + pairs);
             if (!tc::named_all(1, 128, tc::mbar_wait_sleep(&bars[kBarAccFull + acc], use & 1u, err, abort_flag))) break;
             tc::tc_fence_after();
-            const int m0 = (t / geo.tiles_n) * kBM + rank * 128, n0 = (t % geo.tiles_n) * kBN;
+            const Tile at = tile_at(t, geo);
+            const int m0 = at.m + rank * 128, n0 = at.n;
             const float xs = m0 + row < geo.M ? geo.x_scale[m0 + row] : 0.f;
             for (int c = 0; c < kBN / kOutCols && n0 + kOutCols * c < geo.N; ++c, ++chunks) {
                 const uint32_t slot = chunks % kSlots;
@@ -257,7 +290,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     uint4 *at = reinterpret_cast<uint4 *>(stg + tc::sw128(row, q));
                     // N is a multiple of 8: a 16-byte chunk is inside or outside as a whole
                     if (n < geo.N)
-                        *at = finish<F32>(&v[q * (kOutCols / 8) / 32][q * (kOutCols / 8) % 32], xs, n, geo, at);
+                        *at = finish<F32>(&v[q * (kOutCols / 8) / 32][q * (kOutCols / 8) % 32], xs, vec + (n - n0), geo, at);
                 }
                 tc::fence_proxy_async_smem();
                 tc::named_sync(1, 128);
@@ -320,7 +353,8 @@ cudaError_t launch_linear_i8(const LinearI8Args &a, cudaStream_t s)
     geo.N = a.N;
     geo.nk = (a.K + kBK - 1) / kBK;
     geo.tiles_n = (a.N + kBN - 1) / kBN;
-    geo.tiles = (int)(((int64_t)a.M + kBM - 1) / kBM) * geo.tiles_n;
+    geo.tiles_m = (int)(((int64_t)a.M + kBM - 1) / kBM);
+    geo.tiles = geo.tiles_m * geo.tiles_n;
     geo.x_scale = a.x_scale;
     geo.w_scale = a.w_scale;
     geo.bias = a.bias;
