@@ -28,6 +28,10 @@ def _stream_handle(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
+def _handle(stream):
+    return stream if type(stream) is int else _stream_handle(stream)
+
+
 def _ptr(t: Optional[torch.Tensor]) -> ctypes.c_void_p:
     if t is None:
         return ctypes.c_void_p(0)
@@ -72,26 +76,42 @@ def _on(t: torch.Tensor, stream):
             yield stream
 
 
-def _same_device(first: torch.Tensor, **others):
-    for n, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{n} must be on {first.device}, got {t.device}")
+def _elsewhere(t: torch.Tensor, stream) -> bool:
+    """Whether a call on `t` has to switch streams or devices (see _on); otherwise it runs on the
+    current stream as it stands, without the cost of the switch."""
+    return stream is not None or t.get_device() != torch.cuda.current_device()
+
+
+def _current(t: torch.Tensor) -> int:
+    """Handle of the current stream of `t`'s device, which is the current one."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _same_device(first: torch.Tensor, *others):
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"all tensors of a call must be on one device, got {first.device} and {t.device}")
 
 
 def _rows(shape) -> int:
     n = 1
     for s in shape:
-        n *= int(s)
+        n *= s
     return n
 
 
 def _out(out: Optional[torch.Tensor], name: str, shape, dtype, like: torch.Tensor) -> torch.Tensor:
     if out is None:
-        return torch.empty(*shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     _require(out, name, dtype)
-    if tuple(out.shape) != tuple(shape):
+    if out.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(out.shape)}")
-    _same_device(like, **{name: out})
+    _same_device(like, out)
     return out
 
 
@@ -148,27 +168,27 @@ def mate_gate_norm_fwd(y, z, w, eps: float, out, dims: mate_gate_norm_dims, stre
 
 
 def mate_quant_rows_fwd(x, q, scale, dims: mate_quant_dims, stream=None) -> None:
-    rc = _lib.load().mate_quant_rows_fwd(_ptr(x), _ptr(q), _ptr(scale), ctypes.byref(dims), _stream_handle(stream))
+    rc = _lib.load().mate_quant_rows_fwd(_addr(x), _addr(q), _addr(scale), ctypes.byref(dims), _handle(stream))
     check("mate_quant_rows_fwd", rc)
 
 
 def mate_linear_i8_fwd(x, x_scale, w, w_scale, bias, addend, out, dims: mate_linear_i8_dims, stream=None) -> None:
-    rc = _lib.load().mate_linear_i8_fwd(_ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(bias), _ptr(addend),
-                                        _ptr(out), ctypes.byref(dims), _stream_handle(stream))
+    rc = _lib.load().mate_linear_i8_fwd(_addr(x), _addr(x_scale), _addr(w), _addr(w_scale), _addr(bias), _addr(addend),
+                                        _addr(out), ctypes.byref(dims), _handle(stream))
     check("mate_linear_i8_fwd", rc)
 
 
 def mate_gate_norm_i8_fwd(y, z, w, eps: float, q, scale, dims: mate_gate_norm_dims, stream=None) -> None:
-    rc = _lib.load().mate_gate_norm_i8_fwd(_ptr(y), _ptr(z), _ptr(w), float(eps), _ptr(q), _ptr(scale),
-                                           ctypes.byref(dims), _stream_handle(stream))
+    rc = _lib.load().mate_gate_norm_i8_fwd(_addr(y), _addr(z), _addr(w), float(eps), _addr(q), _addr(scale),
+                                           ctypes.byref(dims), _handle(stream))
     check("mate_gate_norm_i8_fwd", rc)
 
 
 def mate_block_norm_fwd(x, y, w_post, gate, w_pre, scale, shift, x_out, h, h_scale, dims: mate_block_norm_dims,
                         stream=None) -> None:
-    rc = _lib.load().mate_block_norm_fwd(_ptr(x), _ptr(y), _ptr(w_post), _ptr(gate), _ptr(w_pre), _ptr(scale),
-                                         _ptr(shift), _ptr(x_out), _ptr(h), _ptr(h_scale), ctypes.byref(dims),
-                                         _stream_handle(stream))
+    rc = _lib.load().mate_block_norm_fwd(_addr(x), _addr(y), _addr(w_post), _addr(gate), _addr(w_pre), _addr(scale),
+                                         _addr(shift), _addr(x_out), _addr(h), _addr(h_scale), ctypes.byref(dims),
+                                         _handle(stream))
     check("mate_block_norm_fwd", rc)
 
 
@@ -293,10 +313,14 @@ def quantize_rows(x, stream=None) -> Codes:
     nn.Linear weight. Returns Codes(q (..., K) int8, scale (...) fp32) with
     scale = max|x| / 127 and q = rint(127 x / max|x|)."""
     _require(x, "x", torch.bfloat16)
-    with _on(x, stream) as st:
-        q = torch.empty_like(x, dtype=torch.int8)
-        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        mate_quant_rows_fwd(x, q, scale, mate_quant_dims(_rows(x.shape[:-1]), int(x.shape[-1]), MATE_BF16), st)
+    if _elsewhere(x, stream):
+        with _on(x, stream):
+            return quantize_rows(x)
+    if x.dim() < 1:
+        raise ValueError("x must be (..., K)")
+    *lead, K = x.shape
+    q, scale = x.new_empty(x.shape, dtype=torch.int8), x.new_empty(lead, dtype=torch.float32)
+    mate_quant_rows_fwd(x, q, scale, mate_quant_dims(_rows(lead), K, MATE_BF16), _current(x))
     return Codes(q, scale)
 
 
@@ -314,22 +338,25 @@ def linear_i8(x_q, x_scale, w_q, w_scale, bias=None, addend=None, out_dtype=torc
     _require(w_scale, "w_scale", torch.float32)
     if w_q.dim() != 2 or x_q.dim() < 1 or x_q.shape[-1] != w_q.shape[1]:
         raise ValueError("x_q must be (..., K) and w_q (N, K)")
-    lead, N = tuple(x_q.shape[:-1]), int(w_q.shape[0])
-    if tuple(x_scale.shape) != lead or tuple(w_scale.shape) != (N,):
+    N, K = w_q.shape
+    shape = x_scale.shape + (N,)
+    if x_q.shape[:-1] != x_scale.shape or w_scale.shape != (N,):
         raise ValueError("x_scale must have one entry per token and w_scale one per row of w_q")
     if bias is not None:
         _require(bias, "bias", torch.float32)
-        if tuple(bias.shape) != (N,):
+        if bias.shape != (N,):
             raise ValueError("bias must have one entry per row of w_q")
     if addend is not None:
         _require(addend, "addend", out_dtype)
-        if tuple(addend.shape) != lead + (N,):
-            raise ValueError(f"addend must have shape {lead + (N,)}")
-    _same_device(x_q, x_scale=x_scale, w_q=w_q, w_scale=w_scale, bias=bias, addend=addend)
-    with _on(x_q, stream) as st:
-        out = _out(out, "out", lead + (N,), out_dtype, x_q)
-        dims = mate_linear_i8_dims(_rows(lead), int(x_q.shape[-1]), N, _DT[out_dtype])
-        mate_linear_i8_fwd(x_q, x_scale, w_q, w_scale, bias, addend, out, dims, st)
+        if addend.shape != shape:
+            raise ValueError(f"addend must have shape {tuple(shape)}")
+    _same_device(x_q, x_scale, w_q, w_scale, bias, addend)
+    if _elsewhere(x_q, stream):
+        with _on(x_q, stream):
+            return linear_i8(x_q, x_scale, w_q, w_scale, bias, addend, out_dtype, out)
+    out = _out(out, "out", shape, out_dtype, x_q)
+    dims = mate_linear_i8_dims(x_scale.numel(), K, N, _DT[out_dtype])
+    mate_linear_i8_fwd(x_q, x_scale, w_q, w_scale, bias, addend, out, dims, _current(x_q))
     return out
 
 
@@ -341,12 +368,13 @@ def gate_norm_i8(y, z, w, group: int, eps: float = 1e-5, stream=None) -> Codes:
     _require(w, "w", torch.float32)
     if z.shape != y.shape or w.shape != (y.shape[-1],):
         raise ValueError("y and z must have one shape and w one entry per channel")
-    _same_device(y, z=z, w=w)
-    with _on(y, stream) as st:
-        q = torch.empty_like(y, dtype=torch.int8)
-        scale = torch.empty(y.shape[:-1], dtype=torch.float32, device=y.device)
-        dims = mate_gate_norm_dims(_rows(y.shape[:-1]), int(y.shape[-1]), int(group), MATE_BF16)
-        mate_gate_norm_i8_fwd(y, z, w, eps, q, scale, dims, st)
+    _same_device(y, z, w)
+    if _elsewhere(y, stream):
+        with _on(y, stream):
+            return gate_norm_i8(y, z, w, group, eps)
+    *lead, C = y.shape
+    q, scale = y.new_empty(y.shape, dtype=torch.int8), y.new_empty(lead, dtype=torch.float32)
+    mate_gate_norm_i8_fwd(y, z, w, eps, q, scale, mate_gate_norm_dims(_rows(lead), C, int(group), MATE_BF16), _current(y))
     return Codes(q, scale)
 
 
@@ -378,15 +406,17 @@ def block_norm(x, y=None, *, w_post=None, gate=None, residual_scale: float = 1.0
     _require(x, "x")
     if x.dtype not in _DT or x.dim() < 2:
         raise ValueError(f"x must be (batch, ..., C) bfloat16 or float32, got {x.dtype}")
-    batch, C = int(x.shape[0]), int(x.shape[-1])
+    batch, *inner, C = x.shape
     if y is not None:
         _require(y, "y", torch.bfloat16)
         if y.shape != x.shape:
             raise ValueError("x and y must have one shape")
+        if w_post is not None and not post_norm:
+            raise ValueError("w_post goes with post_norm")
     for t, n in ((w_post, "w_post"), (w_pre, "w_pre")):
         if t is not None:
             _require(t, n, torch.float32)
-            if tuple(t.shape) != (C,):
+            if t.shape != (C,):
                 raise ValueError(f"{n} must have one entry per channel")
     mod_stride = None
     for t, n in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
@@ -394,25 +424,28 @@ def block_norm(x, y=None, *, w_post=None, gate=None, residual_scale: float = 1.0
             continue
         if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32:
             raise ValueError(f"{n} must be a float32 CUDA tensor")
-        if tuple(t.shape) not in ((batch, C), (C,)) or (C > 1 and t.stride(-1) != 1):
+        if t.shape not in ((batch, C), (C,)) or (C > 1 and t.stride(-1) != 1):
             raise ValueError(f"{n} must be (batch, C) or (C,), its channels contiguous")
-        s = 0 if t.dim() == 1 or batch == 1 else int(t.stride(0))
+        s = 0 if t.dim() == 1 or batch == 1 else t.stride(0)
         if mod_stride not in (None, s):
             raise ValueError("gate, scale and shift must have one stride between batch elements")
         mod_stride = s
-    _same_device(x, y=y, w_post=w_post, gate=gate, w_pre=w_pre, scale=scale, shift=shift, x_out=x_out)
-    with _on(x, stream) as st:
-        h = h_scale = None
-        if y is not None:
-            x_out = _out(x_out, "x_out", x.shape, x.dtype, x)
-        if h_dtype is not None:
-            h = torch.empty(x.shape, dtype=h_dtype, device=x.device)
-            if h_dtype == torch.int8:
-                h_scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        dims = mate_block_norm_dims(batch, _rows(x.shape[1:-1]), C, _NORMS[norm] if post_norm else MATE_NORM_NONE,
-                                    _NORMS[norm], _DT[x.dtype], MATE_I8 if h_dtype == torch.int8 else MATE_BF16,
-                                    mod_stride or 0, float(residual_scale), float(eps))
-        mate_block_norm_fwd(x, y, w_post, gate, w_pre, scale, shift, x_out, h, h_scale, dims, st)
+    _same_device(x, y, w_post, gate, w_pre, scale, shift)
+    if _elsewhere(x, stream):
+        with _on(x, stream):
+            return block_norm(x, y, w_post=w_post, gate=gate, residual_scale=residual_scale, post_norm=post_norm,
+                              w_pre=w_pre, scale=scale, shift=shift, norm=norm, eps=eps, h_dtype=h_dtype, x_out=x_out)
+    h = h_scale = None
+    if y is not None:
+        x_out = _out(x_out, "x_out", x.shape, x.dtype, x)
+    if h_dtype is not None:
+        h = x.new_empty(x.shape, dtype=h_dtype)
+        if h_dtype == torch.int8:
+            h_scale = x.new_empty(x.shape[:-1], dtype=torch.float32)
+    kind = _NORMS[norm]
+    dims = mate_block_norm_dims(batch, _rows(inner), C, kind if post_norm else MATE_NORM_NONE, kind, _DT[x.dtype],
+                                MATE_I8 if h_scale is not None else MATE_BF16, mod_stride or 0, residual_scale, eps)
+    mate_block_norm_fwd(x, y, w_post, gate, w_pre, scale, shift, x_out, h, h_scale, dims, _current(x))
     return x_out, (Codes(h, h_scale) if h_scale is not None else h)
 
 
@@ -586,7 +619,7 @@ def frontend_i8(u: Codes, w_in: Codes, conv_w, conv_b, dt_bias, scan_mode: int, 
                         (conv_b, "conv_b", (dc,)), (dt_bias, "dt_bias", (nheads,))):
         if tuple(t.shape) != shape:
             raise ValueError(f"{n} must have shape {shape}, got {tuple(t.shape)}")
-    _same_device(u.q, u_scale=u.scale, w_in=w_in.q, w_scale=w_in.scale, conv_w=conv_w, conv_b=conv_b, dt_bias=dt_bias)
+    _same_device(u.q, u.scale, w_in.q, w_in.scale, conv_w, conv_b, dt_bias)
     dims = mate_frontend_dims(b, dm, nheads, headdim, ngroups, dstate, MATE_BF16)
     nbytes = mate_frontend_workspace_bytes(T, H, W, dims)
     if nbytes == 0:

@@ -26,13 +26,12 @@ namespace mate {
 
 namespace {
 
-constexpr int kBnThreads = 256;
 constexpr int kBnMaxC = 8192;
 
 // sums over the TPR threads of a row; `turn` counts the calls of the kernel (the
 // partial sums alternate between two buffers, so one barrier per call is enough)
-template <int TPR> struct RowReduce {
-    float *part;  // [2][kBnThreads / 32]
+template <int TPR, int ROWS> struct RowReduce {
+    float *part;  // [2][ROWS * TPR / 32]
     int slot, turn = 0;
 
     __device__ __forceinline__ float sum(float v)
@@ -61,7 +60,7 @@ template <int TPR> struct RowReduce {
     }
     __device__ __forceinline__ float *buffer(float v)
     {
-        float *p = part + (turn & 1) * (kBnThreads / 32) + slot * (TPR / 32);
+        float *p = part + (turn & 1) * (ROWS * TPR / 32) + slot * (TPR / 32);
         ++turn;
         if ((threadIdx.x & 31) == 0) p[(threadIdx.x % TPR) / 32] = v;
         tc::named_sync(1 + slot, TPR);
@@ -69,45 +68,39 @@ template <int TPR> struct RowReduce {
     }
 };
 
-__device__ __forceinline__ void unpack8(const uint4 &u, float (&f)[8])
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ void unpack8(const uint4 &u, float2 (&f)[4])
 {
-    const float2 a = tc::unpack_bf16(u.x), b = tc::unpack_bf16(u.y), c = tc::unpack_bf16(u.z), d = tc::unpack_bf16(u.w);
-    f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y, f[4] = c.x, f[5] = c.y, f[6] = d.x, f[7] = d.y;
+    f[0] = tc::unpack_bf16(u.x), f[1] = tc::unpack_bf16(u.y), f[2] = tc::unpack_bf16(u.z), f[3] = tc::unpack_bf16(u.w);
 }
 
-__device__ __forceinline__ void load8(const float4 *plane, int nv, int v, float (&f)[8])
+__device__ __forceinline__ uint4 pack8(const float2 (&f)[4])
+{
+    return make_uint4(tc::pack_bf16(f[0].x, f[0].y), tc::pack_bf16(f[1].x, f[1].y), tc::pack_bf16(f[2].x, f[2].y),
+                      tc::pack_bf16(f[3].x, f[3].y));
+}
+
+__device__ __forceinline__ void load8(const float4 *plane, int nv, int v, float2 (&f)[4])
 {
     const float4 a = plane[v], b = plane[nv + v];
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w), f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
 }
 
-// TPR threads per row, up to VPL vectors of eight channels per thread
-template <int TPR, int VPL, bool XF32>
-__global__ void __launch_bounds__(kBnThreads, 2) block_norm_kernel(BlockNormArgs a, int blocks_per_item, int rows_per_block)
+// TPR threads per row, up to VPL vectors of eight channels per thread. LAYER: one of the
+// norms is a layer norm (without, no mean is taken or subtracted). The arithmetic runs on
+// packed fp32 pairs: unpacked, the kernel was bound by its issue slots (66% issued, with
+// two CTAs of 128 registers per thread on an SM).
+template <int TPR, int ROWS, int VPL, int CTAS, bool XF32, bool LAYER>
+__global__ void __launch_bounds__(TPR *ROWS, CTAS) block_norm_kernel(BlockNormArgs a, int blocks_per_item, int rows_per_block)
 {
-    constexpr int kRows = kBnThreads / TPR;
     extern __shared__ float4 coef[];
-    __shared__ float part[2 * (kBnThreads / 32)];
+    __shared__ float part[2 * (ROWS * TPR / 32)];
     const int nv = a.C / 8;
     float4 *cg = coef, *ca = coef + 2 * nv, *cs = coef + 4 * nv;
     const int b = blockIdx.x / blocks_per_item, r0 = (blockIdx.x - b * blocks_per_item) * rows_per_block;
     const int r1 = min(a.n, r0 + rows_per_block);
-    {
-        const int64_t m = (int64_t)b * a.mod_stride;
-        float *g = reinterpret_cast<float *>(cg), *w = reinterpret_cast<float *>(ca), *s = reinterpret_cast<float *>(cs);
-        for (int c = threadIdx.x; c < a.C; c += kBnThreads) {
-            const int at = ((c >> 2 & 1) * nv + (c >> 3)) * 4 + (c & 3);
-            if (a.y) g[at] = (a.gate ? a.gate[m + c] : 1.f) * (a.w_post ? a.w_post[c] : 1.f);
-            if (a.h) {
-                w[at] = (a.w_pre ? a.w_pre[c] : 1.f) * (a.scale ? 1.f + a.scale[m + c] : 1.f);
-                s[at] = a.shift ? a.shift[m + c] : 0.f;
-            }
-        }
-    }
-    __syncthreads();
     const int t = threadIdx.x % TPR, slot = threadIdx.x / TPR;
-    RowReduce<TPR> red{part, slot};
-    const float inv_c = 1.f / (float)a.C;
 
     uint4 yv[VPL], xv[XF32 ? 2 * VPL : VPL];
     auto load = [&](int i) {
@@ -129,68 +122,89 @@ __global__ void __launch_bounds__(kBnThreads, 2) block_norm_kernel(BlockNormArgs
             for (int j = 0; j < VPL; ++j) yv[j] = t + j * TPR < nv ? __ldcs(y + t + j * TPR) : make_uint4(0, 0, 0, 0);
         }
     };
-    auto unpack_x = [&](int j, float (&f)[8]) {
+    auto unpack_x = [&](int j, float2 (&f)[4]) {
         if (XF32) {
             const uint4 p = xv[2 * j], q = xv[XF32 ? 2 * j + 1 : 0];
-            f[0] = __uint_as_float(p.x), f[1] = __uint_as_float(p.y), f[2] = __uint_as_float(p.z);
-            f[3] = __uint_as_float(p.w), f[4] = __uint_as_float(q.x), f[5] = __uint_as_float(q.y);
-            f[6] = __uint_as_float(q.z), f[7] = __uint_as_float(q.w);
+            f[0] = make_float2(__uint_as_float(p.x), __uint_as_float(p.y));
+            f[1] = make_float2(__uint_as_float(p.z), __uint_as_float(p.w));
+            f[2] = make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+            f[3] = make_float2(__uint_as_float(q.z), __uint_as_float(q.w));
         } else {
             unpack8(xv[j], f);
         }
     };
     if (r0 + slot < r1) load(r0 + slot);
-    for (int i = r0 + slot; i < r1; i += kRows) {
+    {
+        const int64_t m = (int64_t)b * a.mod_stride;
+        float *g = reinterpret_cast<float *>(cg), *w = reinterpret_cast<float *>(ca), *s = reinterpret_cast<float *>(cs);
+        for (int c = threadIdx.x; c < a.C; c += TPR * ROWS) {
+            const int at = ((c >> 2 & 1) * nv + (c >> 3)) * 4 + (c & 3);
+            if (a.y) g[at] = (a.gate ? a.gate[m + c] : 1.f) * (a.w_post ? a.w_post[c] : 1.f);
+            if (a.h) {
+                w[at] = (a.w_pre ? a.w_pre[c] : 1.f) * (a.scale ? 1.f + a.scale[m + c] : 1.f);
+                s[at] = a.shift ? a.shift[m + c] : 0.f;
+            }
+        }
+    }
+    __syncthreads();
+    RowReduce<TPR, ROWS> red{part, slot};
+    const float inv_c = 1.f / (float)a.C;
+
+    for (int i = r0 + slot; i < r1; i += ROWS) {
         const int64_t row = (int64_t)b * a.n + i, at = row * a.C;
-        float r[VPL][8];
+        float2 r[VPL][4];
         if (a.y) {
             float mu = 0.f, rs = 1.f;
-            if (a.post == MATE_NORM_LAYER) {
-                float s = 0.f;
+            if (LAYER && a.post == MATE_NORM_LAYER) {
+                float2 s = both(0.f);
 #pragma unroll
                 for (int j = 0; j < VPL; ++j) {
-                    float f[8];
+                    float2 f[4];
                     unpack8(yv[j], f);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) s += f[e];
+                    for (int e = 0; e < 4; ++e) s = tc::add_f32x2(s, f[e]);
                 }
-                mu = red.sum(s) * inv_c;
+                mu = red.sum(s.x + s.y) * inv_c;
             }
             if (a.post != MATE_NORM_NONE) {
-                float s = 0.f;
+                float2 s = both(0.f);
 #pragma unroll
                 for (int j = 0; j < VPL; ++j) {
-                    float f[8];
+                    float2 f[4];
                     unpack8(yv[j], f);
-                    if (t + j * TPR < nv) {
+                    if (!LAYER || t + j * TPR < nv) {  // channels past the row are zeros
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) s = fmaf(f[e] - mu, f[e] - mu, s);
+                        for (int e = 0; e < 4; ++e) {
+                            if (LAYER) f[e] = tc::add_f32x2(f[e], both(-mu));
+                            s = tc::fma_f32x2(f[e], f[e], s);
+                        }
                     }
                 }
-                rs = rsqrtf(red.sum(s) * inv_c + a.eps);
+                rs = rsqrtf(red.sum(s.x + s.y) * inv_c + a.eps);
             }
 #pragma unroll
             for (int j = 0; j < VPL; ++j) {
                 const int v = t + j * TPR;
                 if (v < nv) {
-                    float f[8], g[8];
+                    float2 f[4], g[4];
                     unpack8(yv[j], f);
                     load8(cg, nv, v, g);
                     unpack_x(j, r[j]);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) r[j][e] = fmaf((f[e] - mu) * rs, g[e], a.alpha * r[j][e]);
+                    for (int e = 0; e < 4; ++e) {
+                        if (LAYER) f[e] = tc::add_f32x2(f[e], both(-mu));
+                        r[j][e] = tc::fma_f32x2(tc::mul_f32x2(f[e], both(rs)), g[e], tc::mul_f32x2(r[j][e], both(a.alpha)));
+                    }
                     if (XF32) {
                         float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(a.x_out) + at) + 2 * v;
-                        o[0] = make_float4(r[j][0], r[j][1], r[j][2], r[j][3]);
-                        o[1] = make_float4(r[j][4], r[j][5], r[j][6], r[j][7]);
+                        o[0] = make_float4(r[j][0].x, r[j][0].y, r[j][1].x, r[j][1].y);
+                        o[1] = make_float4(r[j][2].x, r[j][2].y, r[j][3].x, r[j][3].y);
                     } else {
-                        reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.x_out) + at)[v] =
-                            make_uint4(tc::pack_bf16(r[j][0], r[j][1]), tc::pack_bf16(r[j][2], r[j][3]),
-                                       tc::pack_bf16(r[j][4], r[j][5]), tc::pack_bf16(r[j][6], r[j][7]));
+                        reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.x_out) + at)[v] = pack8(r[j]);
                     }
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) r[j][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) r[j][e] = both(0.f);
                 }
             }
         } else {
@@ -198,88 +212,100 @@ __global__ void __launch_bounds__(kBnThreads, 2) block_norm_kernel(BlockNormArgs
             for (int j = 0; j < VPL; ++j) unpack_x(j, r[j]);
         }
         // the packed row is used up: the next one's loads run under the rest of this one
-        if (i + kRows < r1) load(i + kRows);
+        if (i + ROWS < r1) load(i + ROWS);
         if (!a.h) continue;
         float mu = 0.f;
-        if (a.pre == MATE_NORM_LAYER) {
-            float s = 0.f;
+        if (LAYER && a.pre == MATE_NORM_LAYER) {
+            float2 s = both(0.f);
 #pragma unroll
             for (int j = 0; j < VPL; ++j)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s += r[j][e];
-            mu = red.sum(s) * inv_c;
+                for (int e = 0; e < 4; ++e) s = tc::add_f32x2(s, r[j][e]);
+            mu = red.sum(s.x + s.y) * inv_c;
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+                if (t + j * TPR < nv) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) r[j][e] = tc::add_f32x2(r[j][e], both(-mu));
+                }
         }
-        float s = 0.f;
+        float2 s = both(0.f);
 #pragma unroll
         for (int j = 0; j < VPL; ++j)
-            if (t + j * TPR < nv) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s = fmaf(r[j][e] - mu, r[j][e] - mu, s);
-            }
-        const float rs = rsqrtf(red.sum(s) * inv_c + a.eps);
+            for (int e = 0; e < 4; ++e) s = tc::fma_f32x2(r[j][e], r[j][e], s);
+        const float rs = rsqrtf(red.sum(s.x + s.y) * inv_c + a.eps);
         float m = 0.f;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
             const int v = t + j * TPR;
             if (v < nv) {
-                float w[8], sh[8];
+                float2 w[4], sh[4];
                 load8(ca, nv, v, w);
                 load8(cs, nv, v, sh);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    r[j][e] = fmaf((r[j][e] - mu) * rs, w[e], sh[e]);
-                    m = i8::amax_nan(m, r[j][e]);
+                for (int e = 0; e < 4; ++e) r[j][e] = tc::fma_f32x2(tc::mul_f32x2(r[j][e], both(rs)), w[e], sh[e]);
+                if (a.h_type == MATE_BF16) {
+                    reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.h) + at)[v] = pack8(r[j]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) m = i8::amax_nan(m, r[j][e]);
                 }
-                if (a.h_type == MATE_BF16)
-                    reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.h) + at)[v] =
-                        make_uint4(tc::pack_bf16(r[j][0], r[j][1]), tc::pack_bf16(r[j][2], r[j][3]),
-                                   tc::pack_bf16(r[j][4], r[j][5]), tc::pack_bf16(r[j][6], r[j][7]));
             }
         }
         if (a.h_type != MATE_I8) continue;
-        const i8::RowScale q = i8::row_scale(red.max(m));
+        const i8::RowScale q = i8::row_scale<false>(red.max(m));
         uint2 *o = reinterpret_cast<uint2 *>(static_cast<int8_t *>(a.h) + at);
+        if (q.pre != 1.f) {  // zero, tiny or not finite (where 0 * v would be NaN)
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) r[j][e] = q.pre == 0.f ? both(0.f) : tc::mul_f32x2(r[j][e], both(q.pre));
+        }
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
             const int v = t + j * TPR;
-            if (v < nv) {
-                if (q.pre != 1.f) {  // zero, tiny or not finite (where 0 * v would be NaN)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) r[j][e] = q.pre == 0.f ? 0.f : r[j][e] * q.pre;
-                }
-                o[v] = make_uint2(i8::codes4(r[j][0], r[j][1], r[j][2], r[j][3], q.mul),
-                                  i8::codes4(r[j][4], r[j][5], r[j][6], r[j][7], q.mul));
-            }
+            if (v < nv) o[v] = make_uint2(i8::codes4(r[j][0], r[j][1], q.mul), i8::codes4(r[j][2], r[j][3], q.mul));
         }
         if (t == 0) a.h_scale[row] = q.scale;
     }
 }
 
-template <int TPR, int VPL, bool XF32> cudaError_t launch(const BlockNormArgs &a, cudaStream_t s)
+template <int TPR, int ROWS, int VPL, int CTAS, bool XF32, bool LAYER>
+cudaError_t launch(const BlockNormArgs &a, cudaStream_t s)
 {
-    constexpr int kRows = kBnThreads / TPR;
+    auto kernel = block_norm_kernel<TPR, ROWS, VPL, CTAS, XF32, LAYER>;
     const size_t smem = (size_t)a.C * 12;
-    cudaError_t e = cudaFuncSetAttribute(block_norm_kernel<TPR, VPL, XF32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kBnMaxC * 12);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBnMaxC * 12);
     if (e != cudaSuccess) return e;
     int dev = 0, nsm = 148;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
-    // one wave of two CTAs per SM, each with its share of one batch element's rows
-    int per_item = std::max(1, std::min((a.n + kRows - 1) / kRows, 2 * nsm / a.batch));
+    // one wave of CTAs, each with its share of one batch element's rows
+    int per_item = std::max(1, std::min((a.n + ROWS - 1) / ROWS, CTAS * nsm / a.batch));
     const int rows = (a.n + per_item - 1) / per_item;
     per_item = (a.n + rows - 1) / rows;
-    block_norm_kernel<TPR, VPL, XF32><<<(unsigned)(per_item * (int64_t)a.batch), kBnThreads, smem, s>>>(a, per_item, rows);
+    kernel<<<(unsigned)(per_item * (int64_t)a.batch), TPR * ROWS, smem, s>>>(a, per_item, rows);
     return cudaGetLastError();
 }
 
-template <bool XF32> cudaError_t dispatch(const BlockNormArgs &a, cudaStream_t s)
+template <bool XF32, bool LAYER> cudaError_t dispatch(const BlockNormArgs &a, cudaStream_t s)
 {
     const int nv = a.C / 8;
-    constexpr int kV = XF32 ? 3 : 5;  // fp32 rows take twice the registers
-    if (nv <= 32 * kV) return launch<32, kV, XF32>(a, s);
-    if (nv <= 64 * kV) return launch<64, kV, XF32>(a, s);
-    if (nv <= 128 * kV) return launch<128, kV, XF32>(a, s);
-    return launch<256, 4, XF32>(a, s);
+    // Measured at 131,072 x 2,560 (after + before, 8-bit h; layer norm with bf16 h): two rows per CTA,
+    // five vectors per thread and three CTAs per SM 383 and 438 us; four rows and two CTAs (128
+    // registers, spills) 418 and 549; five warps per row and two vectors 437 and 549; a warp per
+    // row and ten vectors 411 and 474. fp32 rows take twice the registers: four warps per row and
+    // three vectors 654 us against 680 of two warps and five.
+    if constexpr (XF32) {
+        if (nv <= 32 * 3) return launch<32, 8, 3, 2, XF32, LAYER>(a, s);
+        if (nv <= 64 * 3) return launch<64, 4, 3, 2, XF32, LAYER>(a, s);
+        if (nv <= 128 * 3) return launch<128, 2, 3, 2, XF32, LAYER>(a, s);
+    } else {
+        if (nv <= 32 * 5) return launch<32, 4, 5, 3, XF32, LAYER>(a, s);
+        if (nv <= 64 * 5) return launch<64, 2, 5, 3, XF32, LAYER>(a, s);
+        if (nv <= 128 * 5) return launch<128, 1, 5, 3, XF32, LAYER>(a, s);
+    }
+    return launch<256, 1, 4, 2, XF32, LAYER>(a, s);
 }
 
 }  // namespace
@@ -293,7 +319,9 @@ bool block_norm_supported(const BlockNormArgs &a)
 cudaError_t launch_block_norm(const BlockNormArgs &a, cudaStream_t s)
 {
     Phase ph(MATE_PHASE_BLOCK_NORM, s);
-    return a.x_f32 ? dispatch<true>(a, s) : dispatch<false>(a, s);
+    const bool layer = (a.y && a.post == MATE_NORM_LAYER) || (a.h && a.pre == MATE_NORM_LAYER);
+    if (layer) return a.x_f32 ? dispatch<true, true>(a, s) : dispatch<false, true>(a, s);
+    return a.x_f32 ? dispatch<true, false>(a, s) : dispatch<false, false>(a, s);
 }
 
 }  // namespace mate

@@ -101,10 +101,22 @@ __global__ void __launch_bounds__(kGnThreads) gate_norm_kernel(GateNormArgs a)
 // is a second reduction between the loads and the stores of a row, so a CTA keeps the next
 // row's loads in flight meanwhile: persistent CTAs, and the packed vectors of a row are used
 // up before its sums are.
-template <int VPL> __global__ void __launch_bounds__(kGnThreads) gate_norm_i8_kernel(GateNormArgs a)
+
+// y SiLU(z) on pairs: y z / (1 + 2^(-z log2 e)), each exponential and reciprocal one
+// hardware approximation (2 and 1 fp32 steps)
+__device__ __forceinline__ float2 gated(float2 y, float2 z)
 {
-    __shared__ float ss_vec[VPL * kGnThreads];
-    __shared__ float scale[VPL * kGnThreads];
+    const float2 x = tc::mul_f32x2(z, make_float2(-1.44269504f, -1.44269504f));
+    const float2 d = tc::add_f32x2(make_float2(tc::ex2_approx(x.x), tc::ex2_approx(x.y)), make_float2(1.f, 1.f));
+    return tc::mul_f32x2(tc::mul_f32x2(y, z), make_float2(tc::rcp_approx(d.x), tc::rcp_approx(d.y)));
+}
+
+// ONE: the row is one group, whose sum needs one barrier instead of two.
+template <int VPL, bool ONE>
+__global__ void __launch_bounds__(kGnThreads, VPL <= 2 ? 6 : VPL <= 5 ? 4 : 2) gate_norm_i8_kernel(GateNormArgs a)
+{
+    __shared__ float ss_vec[ONE ? kGnThreads / 32 : VPL * kGnThreads];  // of each vector, or of each warp
+    __shared__ float scale[ONE ? 1 : VPL * kGnThreads];
     __shared__ uint32_t amax[kGnThreads / 32];
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
     const int nv = a.C / 8, gv = a.group / 8, ng = a.C / a.group;
@@ -121,43 +133,55 @@ template <int VPL> __global__ void __launch_bounds__(kGnThreads) gate_norm_i8_ke
     };
     load(blockIdx.x);
     for (int64_t r = blockIdx.x; r < a.M; r += gridDim.x) {
-        float g[VPL][8];
+        float2 g[VPL][4];
+        float ss = 0.f;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
             const uint32_t yw[4] = {yv[j].x, yv[j].y, yv[j].z, yv[j].w};
             const uint32_t zw[4] = {zv[j].x, zv[j].y, zv[j].z, zv[j].w};
-            float s = 0.f;
+            float2 s = make_float2(0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float2 yf = tc::unpack_bf16(yw[e]), zf = tc::unpack_bf16(zw[e]);
-                g[j][2 * e] = yf.x * silu_fast(zf.x);
-                g[j][2 * e + 1] = yf.y * silu_fast(zf.y);
-                s = fmaf(g[j][2 * e], g[j][2 * e], s);
-                s = fmaf(g[j][2 * e + 1], g[j][2 * e + 1], s);
+                g[j][e] = gated(tc::unpack_bf16(yw[e]), tc::unpack_bf16(zw[e]));
+                s = tc::fma_f32x2(g[j][e], g[j][e], s);
             }
-            if (t + j * kGnThreads < nv) ss_vec[t + j * kGnThreads] = s;
+            if (ONE)
+                ss += s.x + s.y;  // vectors past the row are zeros
+            else if (t + j * kGnThreads < nv)
+                ss_vec[t + j * kGnThreads] = s.x + s.y;
         }
         if (r + gridDim.x < a.M) load(r + gridDim.x);
-        __syncthreads();
-        for (int gi = warp; gi < ng; gi += kGnThreads / 32) {
-            float s = 0.f;
-            for (int v = gi * gv + lane; v < (gi + 1) * gv; v += 32) s += ss_vec[v];
-            s = warp_sum(s);
-            if (lane == 0) scale[gi] = rsqrtf(s / (float)a.group + a.eps);
+        float one = 0.f;
+        if (ONE) {
+            ss = warp_sum(ss);
+            if (lane == 0) ss_vec[warp] = ss;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kGnThreads / 32; ++i) one += ss_vec[i];
+            one = rsqrtf(one / (float)a.C + a.eps);
+        } else {
+            __syncthreads();
+            for (int gi = warp; gi < ng; gi += kGnThreads / 32) {
+                float s = 0.f;
+                for (int v = gi * gv + lane; v < (gi + 1) * gv; v += 32) s += ss_vec[v];
+                s = warp_sum(s);
+                if (lane == 0) scale[gi] = rsqrtf(s / (float)a.group + a.eps);
+            }
+            __syncthreads();
         }
-        __syncthreads();
         const float4 *w4 = reinterpret_cast<const float4 *>(a.w);
         float m = 0.f;
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
             const int v = t + j * kGnThreads;
             if (v < nv) {
-                const float f = scale[v / gv];
+                const float f = ONE ? one : scale[v / gv];
                 const float4 wa = w4[2 * v], wb = w4[2 * v + 1];
-                const float wv[8] = {wa.x, wa.y, wa.z, wa.w, wb.x, wb.y, wb.z, wb.w};
+                const float2 wv[4] = {make_float2(wa.x, wa.y), make_float2(wa.z, wa.w), make_float2(wb.x, wb.y),
+                                      make_float2(wb.z, wb.w)};
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    g[j][e] = g[j][e] * f * wv[e];
+                for (int e = 0; e < 4; ++e) {
+                    g[j][e] = tc::mul_f32x2(tc::mul_f32x2(g[j][e], make_float2(f, f)), wv[e]);
                     m = i8::amax_nan(m, g[j][e]);
                 }
             }
@@ -167,19 +191,19 @@ template <int VPL> __global__ void __launch_bounds__(kGnThreads) gate_norm_i8_ke
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kGnThreads / 32; ++i) mb = max(mb, amax[i]);
-        const i8::RowScale rs = i8::row_scale(__uint_as_float(mb));
+        const i8::RowScale rs = i8::row_scale<false>(__uint_as_float(mb));
         uint2 *q = reinterpret_cast<uint2 *>(a.q + r * a.C);
+        if (rs.pre != 1.f) {  // zero, tiny or not finite (where 0 * v would be NaN)
+#pragma unroll
+            for (int j = 0; j < VPL; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    g[j][e] = rs.pre == 0.f ? make_float2(0.f, 0.f) : tc::mul_f32x2(g[j][e], make_float2(rs.pre, rs.pre));
+        }
 #pragma unroll
         for (int j = 0; j < VPL; ++j) {
             const int v = t + j * kGnThreads;
-            if (v < nv) {
-                if (rs.pre != 1.f) {  // zero, tiny or not finite (where 0 * v would be NaN)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) g[j][e] = rs.pre == 0.f ? 0.f : g[j][e] * rs.pre;
-                }
-                q[v] = make_uint2(i8::codes4(g[j][0], g[j][1], g[j][2], g[j][3], rs.mul),
-                                  i8::codes4(g[j][4], g[j][5], g[j][6], g[j][7], rs.mul));
-            }
+            if (v < nv) q[v] = make_uint2(i8::codes4(g[j][0], g[j][1], rs.mul), i8::codes4(g[j][2], g[j][3], rs.mul));
         }
         if (t == 0) a.scale[r] = rs.scale;
     }
@@ -187,10 +211,11 @@ template <int VPL> __global__ void __launch_bounds__(kGnThreads) gate_norm_i8_ke
 
 template <int VPL> cudaError_t launch_i8(const GateNormArgs &a, cudaStream_t s)
 {
+    auto kernel = a.group == a.C ? gate_norm_i8_kernel<VPL, true> : gate_norm_i8_kernel<VPL, false>;
     int dev = 0, nsm = 148, per_sm = 4;
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
-    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, gate_norm_i8_kernel<VPL>, kGnThreads, 0);
-    gate_norm_i8_kernel<VPL><<<std::min(a.M, std::max(1, nsm * per_sm)), kGnThreads, 0, s>>>(a);
+    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kGnThreads, 0);
+    kernel<<<std::min(a.M, std::max(1, nsm * per_sm)), kGnThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 

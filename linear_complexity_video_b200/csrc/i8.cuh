@@ -10,6 +10,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "tc.cuh"
+
 namespace mate {
 namespace i8 {
 
@@ -21,33 +23,43 @@ __device__ __forceinline__ float amax_nan(float m, float v)
     return d;
 }
 
-// What quantises a row: code = rint(v * pre * mul). mul = 127 / amax rounded UP,
-// which makes the codes of bf16 rows exact: rounding of v * mul is done once (a
-// fused multiply-add onto the rounding constant, below), and a tie needs
-// 254 |v| = (2n+1) amax, so 127 divides either amax's 8-bit significand (254: mul is
-// then an exact power of two) or 2n+1 <= 254, that is n = 63, which rounds away from
-// zero as a product slightly above the tie does. Any other product is at least
-// 2^-16 of itself away from a border, and mul's rounding moves it by 2^-23.
+// the same over a pair
+__device__ __forceinline__ float amax_nan(float m, float2 v)
+{
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(m), "f"(v.x), "f"(v.y));
+    return d;
+}
+
+// What quantises a row: code = rint(v * pre * mul).
 struct RowScale {
     float mul, pre, scale;
 };
 
-__device__ __forceinline__ RowScale row_scale(float amax)
+// EXACT: mul = 127 / amax rounded UP, which makes the codes of bf16 rows the correctly
+// rounded ones: the rounding of v * mul is done once (a fused multiply-add onto the
+// rounding constant, below), and a tie needs 254 |v| = (2n+1) amax, so 127 divides either
+// amax's 8-bit significand (254: mul is then an exact power of two) or 2n+1 <= 254, that
+// is n = 63, which rounds away from zero as a product slightly above the tie does. Any
+// other product is at least 2^-16 of itself away from a border, and mul's rounding moves
+// it by 2^-23. Otherwise, for rows of computed fp32 values, which have roundings of their
+// own: mul and scale within 2 fp32 steps, without the two divisions (they were a fifth
+// of the norms' instructions).
+template <bool EXACT> __device__ __forceinline__ RowScale row_scale(float amax)
 {
     RowScale r;
-    if (amax >= 0x1p-100f && amax < __int_as_float(0x7f800000)) {
-        r.mul = __fdiv_ru(127.f, amax);
-        r.pre = 1.f;
-        r.scale = __fdiv_rn(amax, 127.f);
-    } else if (amax > 0.f && amax < 1.f) {  // 127 / amax may overflow: scale the row up first (exact)
-        r.mul = __fdiv_ru(127.f, amax * 0x1p64f);
-        r.pre = 0x1p64f;
+    const bool finite = amax < __int_as_float(0x7f800000);  // false for NaN
+    r.pre = amax >= 0x1p-100f && finite ? 1.f : amax > 0.f && finite ? 0x1p64f : 0.f;
+    if (EXACT) {
+        r.mul = r.pre != 0.f ? __fdiv_ru(127.f, amax * r.pre) : 0.f;
         r.scale = __fdiv_rn(amax, 127.f);
     } else {
-        r.mul = 0.f;
-        r.pre = 0.f;
-        r.scale = amax == 0.f ? 0.f : __int_as_float(0x7fc00000);
+        float inv;  // of a normal number; results below 2^-126 kept
+        asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(amax * r.pre));
+        r.mul = r.pre != 0.f ? 127.f * inv : 0.f;
+        r.scale = amax * (1.f / 127.f);
     }
+    if (!finite) r.scale = __int_as_float(0x7fc00000);
     return r;
 }
 
@@ -56,11 +68,12 @@ __device__ __forceinline__ RowScale row_scale(float amax)
 constexpr float kRound = 12582912.f;
 
 // four codes, the first in the low byte
-__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float mul)
+__device__ __forceinline__ uint32_t codes4(float2 a, float2 b, float mul)
 {
-    const uint32_t x = __float_as_uint(fmaf(a, mul, kRound)), y = __float_as_uint(fmaf(b, mul, kRound));
-    const uint32_t z = __float_as_uint(fmaf(c, mul, kRound)), w = __float_as_uint(fmaf(d, mul, kRound));
-    return __byte_perm(__byte_perm(x, y, 0x0040), __byte_perm(z, w, 0x0040), 0x5410);
+    const float2 m = make_float2(mul, mul), k = make_float2(kRound, kRound);
+    const float2 x = tc::fma_f32x2(a, m, k), y = tc::fma_f32x2(b, m, k);
+    return __byte_perm(__byte_perm(__float_as_uint(x.x), __float_as_uint(x.y), 0x0040),
+                       __byte_perm(__float_as_uint(y.x), __float_as_uint(y.y), 0x0040), 0x5410);
 }
 
 }  // namespace i8

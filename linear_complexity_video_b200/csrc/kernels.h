@@ -209,6 +209,9 @@ bool quant_rows_supported(const QuantArgs &a);
 cudaError_t launch_quant_rows(const QuantArgs &a, cudaStream_t s);
 bool linear_i8_supported(const LinearI8Args &a);
 cudaError_t launch_linear_i8(const LinearI8Args &a, cudaStream_t s);
+// its form for few tokens (linear_i8_few.cu), which launch_linear_i8 chooses
+bool linear_i8_few_wanted(const LinearI8Args &a, int nsm);
+cudaError_t launch_linear_i8_few(const LinearI8Args &a, int nsm, cudaStream_t s);
 bool block_norm_supported(const BlockNormArgs &a);
 cudaError_t launch_block_norm(const BlockNormArgs &a, cudaStream_t s);
 // tensor-core bi-SSD path (bf16, head dim 64, d_state 64, both directions)

@@ -338,10 +338,13 @@ bool linear_i8_supported(const LinearI8Args &a)
 
 cudaError_t launch_linear_i8(const LinearI8Args &a, cudaStream_t s)
 {
+    int dev = 0, nsm = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
+    if (!tmap_available()) return cudaErrorNotSupported;
+    if (linear_i8_few_wanted(a, nsm)) return launch_linear_i8_few(a, nsm, s);
     auto kernel = a.out_f32 ? linear_i8_kernel<true> : linear_i8_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e != cudaSuccess) return e;
-    if (!tmap_available()) return cudaErrorNotSupported;
     const TmapType ot = a.out_f32 ? TmapType::f32 : TmapType::bf16;
     const int oc = a.out_f32 ? 32 : 64;
     CUtensorMap ma, mb, mo, md;
@@ -359,8 +362,6 @@ cudaError_t launch_linear_i8(const LinearI8Args &a, cudaStream_t s)
     geo.w_scale = a.w_scale;
     geo.bias = a.bias;
     geo.has_addend = a.addend != nullptr;
-    int dev = 0, nsm = 148;
-    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
     const int grid = 2 * std::min(geo.tiles, std::max(nsm / 2, 1));
     Phase ph(a.phase ? a.phase : MATE_PHASE_LINEAR_I8, s);
     kernel<<<grid, kThreads, kSmemBytes, s>>>(ma, mb, mo, md, geo, a.err);

@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kQThreads) quant_rows_kernel(QuantArgs a)
 #pragma unroll
         for (int i = 0; i < kWarps; ++i) m = max(m, part[slot * kWarps + i]);
     }
-    const i8::RowScale rs = i8::row_scale(__uint_as_float(m << 16));
+    const i8::RowScale rs = i8::row_scale<true>(__uint_as_float(m << 16));
     if (!live) return;
     uint2 *q = reinterpret_cast<uint2 *>(a.q + row * a.K);
     if (rs.pre != 1.f) {  // zero, tiny or not finite (where 0 * v would be NaN)
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kQThreads) quant_rows_kernel(QuantArgs a)
         if (t + j * TPR < nv) {
             const float2 f0 = tc::unpack_bf16(v[j].x), f1 = tc::unpack_bf16(v[j].y), f2 = tc::unpack_bf16(v[j].z),
                          f3 = tc::unpack_bf16(v[j].w);
-            q[t + j * TPR] = make_uint2(i8::codes4(f0.x, f0.y, f1.x, f1.y, rs.mul), i8::codes4(f2.x, f2.y, f3.x, f3.y, rs.mul));
+            q[t + j * TPR] = make_uint2(i8::codes4(f0, f1, rs.mul), i8::codes4(f2, f3, rs.mul));
         }
     }
     if (t == 0) a.scale[row] = rs.scale;

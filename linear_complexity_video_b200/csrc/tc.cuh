@@ -411,6 +411,14 @@ __device__ __forceinline__ float ex2_approx(float x)
     return y;
 }
 
+// 1 / x by the hardware approximation (flush-to-zero; 1/inf = +0).
+__device__ __forceinline__ float rcp_approx(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -524,6 +532,17 @@ __device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank)
     uint32_t a;
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
     return a;
+}
+
+// 16 bytes of another CTA's shared memory (a cluster_addr)
+__device__ __forceinline__ int4 ld_cluster(uint32_t addr)
+{
+    int4 v;
+    asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
 }
 
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_addr)
