@@ -466,8 +466,9 @@ def modulation(c, w: Codes, bias=None, stream=None) -> torch.Tensor:
     """A layer's modulation vectors from its conditioning, as an 8-bit linear layer with fp32
     output. c: (batch, K) bf16; w: Codes of (3 d_model, K); bias: (3 d_model,) fp32. Returns
     (batch, 3 d_model): shift, scale and gate, as stack() takes them."""
-    x = quantize_rows(c, stream=stream)
-    return linear_i8(x.q, x.scale, w.q, w.scale, bias=bias, out_dtype=torch.float32, stream=stream)
+    _require(c, "c", torch.bfloat16)
+    with _on(c, stream):
+        return linear_i8(*quantize_rows(c), *w, bias=bias, out_dtype=torch.float32)
 
 
 def block(u, weights, *, scan_mode: int, review_pool, chunk: int, nheads: int, headdim: int, ngroups: int,
@@ -485,9 +486,15 @@ def block(u, weights, *, scan_mode: int, review_pool, chunk: int, nheads: int, h
     block_norm's h) and is quantised per token otherwise, the gated norm and the TESA output
     become Codes too, and the scan and the attention run in bf16 as above."""
     w = weights
-    if isinstance(w["w_in"], Codes):
-        return _block_i8(u, w, scan_mode, review_pool, chunk, nheads, headdim, ngroups, dstate, attn_heads, attn_dim, Tw,
-                         Sw, shift, eps, stream, keep)
+    eight = [isinstance(w[n], Codes) for n in _PROJECTIONS]
+    if any(eight):
+        if not all(eight):
+            raise ValueError("the weights of all the block's matrix products must be Codes, or none (quantize_block)")
+        with _on(u.q if isinstance(u, Codes) else u, stream):
+            return _block_i8(u, w, scan_mode, review_pool, chunk, nheads, headdim, ngroups, dstate, attn_heads, attn_dim,
+                             Tw, Sw, shift, eps, keep)
+    if isinstance(u, Codes):
+        raise ValueError("u is Codes: the weights must be 8-bit too (quantize_block)")
     b, T, H, W, _ = u.shape
     z, x, dt, B, C = frontend(u, w["w_in"], w["conv_w"], w["conv_b"], w["dt_bias"], scan_mode, nheads, headdim,
                               ngroups, dstate, stream=stream)
@@ -503,25 +510,24 @@ def block(u, weights, *, scan_mode: int, review_pool, chunk: int, nheads: int, h
 
 
 def _block_i8(u, w, scan_mode, review_pool, chunk, nheads, headdim, ngroups, dstate, attn_heads, attn_dim, Tw, Sw, shift,
-              eps, stream, keep):
+              eps, keep):
     if not isinstance(u, Codes):
-        u = quantize_rows(u, stream=stream)
-    with _on(u.q, stream) as st:
-        b, T, H, W, _ = u.q.shape
-        z, x, dt, B, C = frontend_i8(u, w["w_in"], w["conv_w"], w["conv_b"], w["dt_bias"], scan_mode, nheads, headdim,
-                                     ngroups, dstate, stream=st)
-        y = bissd(x, dt, w["A"], B, C, w["D"], scan_mode, review_pool, chunk=chunk, stream=st)
-        d_inner = nheads * headdim
-        y_ma = gate_norm_i8(y.view(b, T, H, W, d_inner), z, w["norm_w"], d_inner // ngroups, eps, stream=st)
-        q, k, v = (linear_i8(*u, *w[n], stream=st).view(b, T, H, W, attn_heads, attn_dim) for n in ("w_q", "w_k", "w_v"))
-        y_te = tesa(q, k, v, Tw, Sw, shift, stream=st)
-        c_te = quantize_rows(y_te.view(b, T, H, W, attn_heads * attn_dim), stream=st)
-        # the branches' codes have scales of their own: the second product adds the first
-        out = linear_i8(*c_te, *w["w_te"], stream=st)
-        linear_i8(*y_ma, *w["w_ma"], addend=out, out=out, stream=st)
+        u = quantize_rows(u)
+    b, T, H, W, _ = u.q.shape
+    z, x, dt, B, C = frontend_i8(u, w["w_in"], w["conv_w"], w["conv_b"], w["dt_bias"], scan_mode, nheads, headdim,
+                                 ngroups, dstate)
+    y = bissd(x, dt, w["A"], B, C, w["D"], scan_mode, review_pool, chunk=chunk)
+    d_inner = nheads * headdim
+    y_ma = gate_norm_i8(y.view(b, T, H, W, d_inner), z, w["norm_w"], d_inner // ngroups, eps)
+    q, k, v = (linear_i8(*u, *w[n]).view(b, T, H, W, attn_heads, attn_dim) for n in ("w_q", "w_k", "w_v"))
+    y_te = tesa(q, k, v, Tw, Sw, shift)
+    c_te = quantize_rows(y_te.view(b, T, H, W, attn_heads * attn_dim))
+    # the branches' codes have scales of their own: the second product adds the first
+    te = linear_i8(*c_te, *w["w_te"])
     if keep:
-        return out, dict(u=u, z=z, x=x, dt=dt, B=B, C=C, y=y, y_ma=y_ma, q=q, k=k, v=v, y_te=y_te, c_te=c_te)
-    return out
+        out = linear_i8(*y_ma, *w["w_ma"], addend=te)
+        return out, dict(u=u, z=z, x=x, dt=dt, B=B, C=C, y=y, y_ma=y_ma, q=q, k=k, v=v, y_te=y_te, c_te=c_te, te=te)
+    return linear_i8(*y_ma, *w["w_ma"], addend=te, out=te)
 
 
 def stack(x, layers, *, norm: str = "rms", residual_scale: float = 1.0, norm_eps: float = 1e-6, stream=None, **spec):
@@ -537,19 +543,21 @@ def stack(x, layers, *, norm: str = "rms", residual_scale: float = 1.0, norm_eps
     layers = [tuple(ly) + ({},) * (3 - len(ly)) for ly in layers]
     if not layers:
         return x
-    with _on(x, stream) as st:
-        C = int(x.shape[-1])
-        kw = dict(norm=norm, eps=norm_eps, stream=st)
+    C = int(x.shape[-1])
+    for _, mod, _ in layers:
+        if tuple(mod.shape) != (x.shape[0], 3 * C):
+            raise ValueError(f"mod must be (batch, 3 d_model) = {(int(x.shape[0]), 3 * C)}, got {tuple(mod.shape)}")
+    kw = dict(norm=norm, eps=norm_eps)
 
-        def pre(ly):
-            w, mod, _ = ly
-            return dict(w_pre=w.get("w_pre"), shift=mod[:, :C], scale=mod[:, C:2 * C],
-                        h_dtype=torch.int8 if isinstance(w["w_in"], Codes) else torch.bfloat16)
+    def before(w, mod, _):
+        return dict(w_pre=w.get("w_pre"), shift=mod[:, :C], scale=mod[:, C:2 * C],
+                    h_dtype=torch.int8 if isinstance(w["w_in"], Codes) else torch.bfloat16)
 
-        _, h = block_norm(x, **pre(layers[0]), **kw)
+    with _on(x, stream):
+        _, h = block_norm(x, **before(*layers[0]), **kw)
         for i, (w, mod, over) in enumerate(layers):
-            y = block(h, w, stream=st, **{**spec, **over})
-            after = pre(layers[i + 1]) if i + 1 < len(layers) else dict(h_dtype=None)
+            y = block(h, w, **{**spec, **over})
+            after = before(*layers[i + 1]) if i + 1 < len(layers) else dict(h_dtype=None)
             x, h = block_norm(x, y, w_post=w.get("w_post"), gate=mod[:, 2 * C:], residual_scale=residual_scale, **after,
                               **kw)
     return x

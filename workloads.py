@@ -170,6 +170,23 @@ def generate_block(cfg: Config, seed: int = 0, d_model: int = D_MODEL) -> Dict[s
     return out
 
 
+def generate_layer(cfg: Config, seed: int = 0, d_model: int = D_MODEL) -> Dict[str, torch.Tensor]:
+    """One residual layer around the token mixer on the host: generate_block's tensors, then, from
+    a generator seeded with seed + 6 in this order, the norm weights w_pre, w_post ~ 1 + N(0, 1) / 10
+    fp32, the modulation's w_mod ~ N(0, 1 / d_model) (3 d_model, d_model) and a conditioning vector
+    c ~ N(0, 1) per batch element, bf16, and its bias b_mod fp32: shift and scale 0, gate 1 (each layer
+    starts as a plain pre- and post-norm residual layer with a modulation of unit spread around it)."""
+    out = generate_block(cfg, seed=seed, d_model=d_model)
+    g = torch.Generator().manual_seed(seed + 6)
+    w_pre, w_post = (1.0 + torch.randn(d_model, generator=g) / 10 for _ in range(2))
+    w_mod = torch.randn(3 * d_model, d_model, generator=g) / math.sqrt(d_model)
+    c = torch.randn(cfg.batch, d_model, generator=g)
+    b_mod = torch.cat([torch.zeros(2 * d_model), torch.ones(d_model)])
+    out.update(w_pre=w_pre.float(), w_post=w_post.float(), w_mod=w_mod.to(torch.bfloat16), c=c.to(torch.bfloat16),
+               b_mod=b_mod.float())
+    return out
+
+
 def sweep_configs():
     """N from 8k to 131k tokens at H=W=32 with the 131k grid's other settings."""
     base = CONFIGS[HEADLINE]
