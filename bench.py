@@ -3,7 +3,7 @@ prefix scan, the bidirectional SSD scan and TESA over one batch of a
 synthetic latent grid.
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--config NAME] [--impl mate|reference]
-    python bench.py --report | --component compose|frontend|gate_norm|block [--config NAME]
+    python bench.py --report | --component compose|frontend|gate_norm|block|block_i8|stack [--config NAME]
 
 Prints one JSON line (rank 0). With N > 1 (torchrun, one rank per GPU; a
 plain `python bench.py --gpus N` starts the N ranks itself) every rank
@@ -555,25 +555,27 @@ def time_gate_norm(cfg, steps, warmup, sample_rows=256):
             "oracle_s_scaled": round(t_or, 2), "oracle_sample_rows": sample_rows}
 
 
-def time_block(cfg, steps, warmup):
-    """One MATE token mixer (api.block: front-end, bi-SSD, gated norm, TE-branch q/k/v
-    projections, TESA, composition) on the grid with model width 2560: device time from
-    CUDA events, the split by phase from the phase hook (the mean over several hooked
-    calls), and the dense GEMMs' rate (in_proj, q/k/v, composition) against the burst
-    bf16 peak."""
+def mixer_spec(cfg):
+    """api.block's arguments for a config."""
+    return dict(scan_mode=cfg.modes[0], review_pool=cfg.review, chunk=cfg.chunk, nheads=cfg.nheads,
+                headdim=cfg.headdim, ngroups=cfg.ngroups, dstate=cfg.dstate, attn_heads=cfg.attn_heads,
+                attn_dim=cfg.attn_dim, Tw=cfg.Tw, Sw=cfg.Sw, shift=cfg.shift)
+
+
+def mixer_gemm_flops(cfg):
+    """Multiply-adds (twice) of one token mixer's matrix products: in_proj, q/k/v, composition."""
+    d_inner, te = cfg.nheads * cfg.headdim, cfg.attn_heads * cfg.attn_dim
+    dc = d_inner + 2 * cfg.ngroups * cfg.dstate
+    return 2.0 * cfg.tokens * workloads.D_MODEL * ((d_inner + dc + cfg.nheads) + 3 * te + (d_inner + te))
+
+
+def time_call(call, steps, warmup):
+    """Milliseconds per call from CUDA events, the split by phase from the phase hook (the mean
+    over several hooked calls) and the clocks during the timed region."""
     import torch
 
     import linear_complexity_video_b200 as mate
     from linear_complexity_video_b200 import _lib
-
-    host = workloads.generate_block(cfg, seed=0)
-    d = {k: v.cuda() for k, v in host.items()}
-    spec = dict(scan_mode=cfg.modes[0], review_pool=cfg.review, chunk=cfg.chunk, nheads=cfg.nheads,
-                headdim=cfg.headdim, ngroups=cfg.ngroups, dstate=cfg.dstate, attn_heads=cfg.attn_heads,
-                attn_dim=cfg.attn_dim, Tw=cfg.Tw, Sw=cfg.Sw, shift=cfg.shift)
-
-    def call():
-        return mate.block(d["u"], d, **spec)
 
     for _ in range(warmup):
         out = call()
@@ -614,22 +616,70 @@ def time_block(cfg, steps, warmup):
         else:
             name = _lib.PHASES[ph]
             phases[name] = phases.get(name, 0.0) + opened.pop(ph).elapsed_time(ev) / hooked
-    dm = workloads.D_MODEL
-    d_inner, te = cfg.nheads * cfg.headdim, cfg.attn_heads * cfg.attn_dim
-    dc = d_inner + 2 * cfg.ngroups * cfg.dstate
-    gemm = 2.0 * cfg.tokens * dm * ((d_inner + dc + cfg.nheads) + 3 * te + (d_inner + te))
-    gemm_ms = phases.get("front_proj", 0.0) + phases.get("compose", 0.0)
+    del out
+    return ms, phases, clocks
+
+
+def time_block(cfg, steps, warmup, eight=False):
+    """One MATE token mixer (api.block: front-end, bi-SSD, gated norm, TE-branch q/k/v
+    projections, TESA, composition) on the grid with model width 2560: device time from
+    CUDA events, the split by phase, and the dense products' rate (in_proj, q/k/v,
+    composition) against the measured bf16 peaks, or in 8 bits (eight: quantize_block's
+    weights) against twice those."""
+    import torch
+
+    import linear_complexity_video_b200 as mate
+
+    host = workloads.generate_block(cfg, seed=0)
+    d = {k: v.cuda() for k, v in host.items()}
+    u, w = d["u"], mate.quantize_block(d) if eight else d
+    if eight:
+        u = mate.quantize_rows(u)
+    spec = mixer_spec(cfg)
+    ms, phases, clocks = time_call(lambda: mate.block(u, w, **spec), steps, warmup)
+    gemm = mixer_gemm_flops(cfg)
+    gemm_ms = phases.get("front_proj", 0.0) + phases.get("linear_i8" if eight else "compose", 0.0)
     peaks, _ = load_peaks()
-    del d, out
+    peak, sustained = ((2 if eight else 1) * float(peaks[k]) for k in ("bf16_tflops", "bf16_tflops_sustained"))
+    del d, u, w
     torch.cuda.empty_cache()
-    return {"report": "block", "workload": cfg.name, "scan": workloads.MODE_NAMES[cfg.modes[0]], "tokens": cfg.tokens,
-            "d_model": dm, "ms": round(ms, 4), "mtokens_per_s": round(cfg.tokens / ms / 1e3, 2),
+    rate = gemm / (gemm_ms / 1e3) / 1e12 if gemm_ms else None
+    return {"report": "block_i8" if eight else "block", "workload": cfg.name,
+            "scan": workloads.MODE_NAMES[cfg.modes[0]], "tokens": cfg.tokens,
+            "d_model": workloads.D_MODEL, "ms": round(ms, 4), "mtokens_per_s": round(cfg.tokens / ms / 1e3, 2),
             "phase_ms": {k: round(v, 4) for k, v in phases.items()},
             "gemm_tflop": round(gemm / 1e12, 3),
-            "gemm_tflops": round(gemm / (gemm_ms / 1e3) / 1e12, 1) if gemm_ms else None,
-            "gemm_tensor_frac": round(gemm / (gemm_ms / 1e3) / 1e12 / float(peaks["bf16_tflops"]), 4) if gemm_ms else None,
-            "gemm_tensor_frac_sustained": round(gemm / (gemm_ms / 1e3) / 1e12 / float(peaks["bf16_tflops_sustained"]), 4)
-            if gemm_ms else None, "clocks": clocks}
+            "gemm_tflops": round(rate, 1) if rate else None,
+            "gemm_tensor_frac": round(rate / peak, 4) if rate else None,
+            "gemm_tensor_frac_sustained": round(rate / sustained, 4) if rate else None, "clocks": clocks}
+
+
+def time_block_i8(cfg, steps, warmup):
+    """time_block with every matrix product in 8 bits."""
+    return time_block(cfg, steps, warmup, eight=True)
+
+
+def time_stack(cfg, steps, warmup):
+    """Two residual layers around the token mixer (api.stack: norm before, token mixer, norm after
+    with gate and residual, the joint between the layers in one pass) on the grid, in bf16 and in
+    8 bits: device time per layer and the norms' share."""
+    import torch
+
+    import linear_complexity_video_b200 as mate
+
+    host = workloads.generate_layer(cfg, seed=0)
+    d = {k: v.cuda() for k, v in host.items()}
+    mod = mate.modulation(d["c"], mate.quantize_rows(d["w_mod"]), d["b_mod"])
+    spec = mixer_spec(cfg)
+    out = {"report": "stack", "workload": cfg.name, "tokens": cfg.tokens, "d_model": workloads.D_MODEL, "layers": 2}
+    for name, w in (("bf16", d), ("i8", mate.quantize_block(d))):
+        layers = [(w, mod), (w, mod)]
+        ms, phases, clocks = time_call(lambda: mate.stack(d["u"], layers, **spec), steps, warmup)
+        out[name] = {"ms_per_layer": round(ms / 2, 4), "mtokens_per_s": round(2 * cfg.tokens / ms / 1e3, 2),
+                     "phase_ms": {k: round(v, 4) for k, v in phases.items()}, "clocks": clocks}
+    del d, layers
+    torch.cuda.empty_cache()
+    return out
 
 
 def time_frontend(cfg, steps, warmup):
@@ -762,6 +812,8 @@ def run_report(args):
     print(json.dumps(time_frontend(cfg, args.steps, args.warmup)), flush=True)
     print(json.dumps(time_gate_norm(cfg, args.steps, args.warmup)), flush=True)
     print(json.dumps(time_block(cfg, args.steps, args.warmup)), flush=True)
+    print(json.dumps(time_block_i8(cfg, args.steps, args.warmup)), flush=True)
+    print(json.dumps(time_stack(cfg, args.steps, args.warmup)), flush=True)
     Ns, ts = [], []
     for cfg in workloads.sweep_configs():
         ms, phases = time_config(cfg, cfg.modes[0], args.steps, args.warmup)
@@ -897,7 +949,7 @@ def main():
     ap.add_argument("--chunk", type=int, default=0, help="override the scan chunk length (a tiling choice)")
     ap.add_argument("--report", action="store_true",
                     help="time every bf16 grid in each of its scan orders and the N sweep (one JSON line each)")
-    ap.add_argument("--component", choices=["compose", "frontend", "gate_norm", "block"],
+    ap.add_argument("--component", choices=["compose", "frontend", "gate_norm", "block", "block_i8", "stack"],
                     help="time one component beside the token mix on --config (one JSON line)")
     ap.add_argument("--steps-ref", type=int, default=1)
     ap.add_argument("--warmup-ref", type=int, default=0)
@@ -928,7 +980,7 @@ def main():
         return
     if args.component:
         fn = {"compose": time_compose, "frontend": time_frontend, "gate_norm": time_gate_norm,
-              "block": time_block}[args.component]
+              "block": time_block, "block_i8": time_block_i8, "stack": time_stack}[args.component]
         print(json.dumps(fn(cfg, args.steps, args.warmup)), flush=True)
         return
 
