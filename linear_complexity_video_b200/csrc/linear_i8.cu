@@ -5,19 +5,23 @@
 // 127 * 127 * K below 2^31. The two scales, the bias and the addend are applied to it
 // in fp32 in the epilogue, and the result is rounded once to the output type.
 //
-// Persistent CTA pairs (clusters of two, cta_group::2), 192 threads per CTA; a pair
-// computes output tiles of 256 x 256, CTA r the rows 128 r ..:
-//   warp 0    TMA loads of the CTA's 128 x 128 codes of x and its half, 128 x 128, of
-//             the w tile into a 5-stage ring (32 KB per stage and CTA, 128-byte
-//             swizzle, K-major; codes past K, M or N load as zeros), all completing on
-//             the barriers of rank 0;
+// Persistent CTA pairs (clusters of two, cta_group::2), 320 threads per CTA; a pair
+// computes output tiles of 256 x 256 (or 192 or 128 columns, tile_width), CTA r the
+// rows 128 r ..:
+//   warp 0    TMA loads of the CTA's 128 x 128 codes of x and its half of the w tile
+//             into a 5-stage ring (32 KB per stage and CTA, 128-byte swizzle,
+//             K-major; codes past K, M or N load as zeros), all completing on the
+//             barriers of rank 0;
 //   warp 1    TMEM allocation and, in rank 0, tcgen05.mma issue: four M = 256, N = 256,
 //             K = 32 MMAs per stage into one of two TMEM accumulators (2 x 256 columns
 //             in each CTA), so that a tile's epilogue runs while the next accumulates;
-//   warps 2-5 the epilogue: TMEM -> registers -> scales, bias, addend -> a staging tile
-//             of 128 rows x 128 bytes in the 128-byte swizzle (three in turn) -> TMA
-//             store. The addend arrives in the staging tile by TMA, two tiles ahead; the
-//             columns' scales and bias wait in shared memory, fetched a tile ahead.
+//   warps 2-9 the epilogue, two groups of four warps that take the tile's column chunks
+//             alternately: TMEM -> registers -> scales, bias, addend -> a staging tile
+//             of 128 rows x 128 bytes in the 128-byte swizzle (two per group) -> TMA
+//             store. The addend arrives in the staging tile by TMA, a chunk ahead; the
+//             columns' scales and bias wait in shared memory, fetched a tile ahead
+//             (read from global memory chunk by chunk they cost in_proj of 131,072
+//             tokens 3.20 ms instead of 2.48).
 // A pair reads 64 KB for the work that two single CTAs would read 96 KB for: the pair
 // halves each CTA's share of w. Tiles are walked in groups of eight tile rows, so that the
 // 74 pairs at work read about eight rows' x and nine columns' w.
@@ -37,28 +41,31 @@ namespace mate {
 
 namespace {
 
-constexpr int kBM = 256, kBN = 256, kBK = 128;       // tile of a pair; a K step is 128 codes = one swizzled row
-constexpr int kStages = 5, kSlots = 3;
+constexpr int kBM = 256, kBK = 128;                  // rows of a pair's tile; a K step is 128 codes = one swizzled row
+constexpr int kMaxBN = 256;                          // columns of a tile, at most
+constexpr int kStages = 5, kGroups = 2, kSlots = 2;  // staging tiles per epilogue group
 constexpr int kGroup = 8;                            // tile rows walked together
 constexpr uint32_t kTile = 128 * kBK;                // 16 KB: one CTA's part of x or w
 constexpr uint32_t kStage = 2 * kTile;
 constexpr uint32_t kOutTile = 128 * 128;             // 16 KB: 128 rows x 128 bytes
 constexpr uint32_t kOffStages = 0;
 constexpr uint32_t kOffOut = kStages * kStage;
-constexpr uint32_t kOffVec = kOffOut + kSlots * kOutTile;  // w_scale and bias of the tile's columns
-constexpr uint32_t kOffBar = kOffVec + 2 * kBN * 4;
+constexpr uint32_t kOffVec = kOffOut + kGroups * kSlots * kOutTile;  // per group: w_scale and bias of its columns
+constexpr uint32_t kOffBar = kOffVec + 2 * kMaxBN * 4;
 // full, empty (per stage), acc_full[2], acc_empty[2], addend (per slot), drain; then the TMEM slot and the abort flag
 constexpr int kBarFull = 0, kBarEmpty = kStages, kBarAccFull = 2 * kStages, kBarAccEmpty = 2 * kStages + 2,
-              kBarAdd = 2 * kStages + 4, kBarDrain = kBarAdd + kSlots, kNumBars = kBarDrain + 1;
+              kBarAdd = 2 * kStages + 4, kBarDrain = kBarAdd + kGroups * kSlots, kNumBars = kBarDrain + 1;
 constexpr uint32_t kOffMisc = kOffBar + 8 * kNumBars;
-constexpr uint32_t kSmemBytes = kOffMisc + 16 + 1024;  // + alignment slack
+constexpr uint32_t kSmemBytes = kOffMisc + 16;
 static_assert(kSmemBytes <= 227 * 1024, "linear_i8: shared memory");
-constexpr int kThreads = 192;
+constexpr int kThreads = 64 + 128 * kGroups;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxK = 131072;
+static_assert(kOffBar % 8 == 0 && kOffVec % 16 == 0, "linear_i8: alignment");
 
 struct Geo {
     int M, N, nk;        // rows, columns, 128-wide K steps
+    int bn;              // columns of a tile: 256, 192 or 128
     int tiles_m, tiles_n, tiles;  // output tiles along M, along N, in total
     const float *x_scale, *w_scale, *bias;
     int has_addend;
@@ -73,11 +80,11 @@ __device__ __forceinline__ Tile tile_at(int t, const Geo &geo)
 {
     const int g = t / (kGroup * geo.tiles_n), r = t - g * kGroup * geo.tiles_n;
     const int rows = min(kGroup, geo.tiles_m - g * kGroup);
-    return {(g * kGroup + r % rows) * kBM, (r / rows) * kBN};
+    return {(g * kGroup + r % rows) * kBM, (r / rows) * geo.bn};
 }
 
 // eight (bf16) or four (fp32) outputs, one 16-byte chunk of a staging tile: `acc` scaled, plus
-// the bias (`vec`: the columns' w_scale, their bias kBN floats on) and the addend that `stg` holds
+// the bias (`vec`: the columns' w_scale, their bias 128 floats on) and the addend that `stg` holds
 template <bool F32>
 __device__ __forceinline__ uint4 finish(const uint32_t *acc, float xs, const float *vec, const Geo &geo, const uint4 *stg)
 {
@@ -91,7 +98,7 @@ __device__ __forceinline__ uint4 finish(const uint32_t *acc, float xs, const flo
         v[4 * q + 2] = (float)(int)acc[4 * q + 2] * xs * ws.z;
         v[4 * q + 3] = (float)(int)acc[4 * q + 3] * xs * ws.w;
         if (geo.bias) {
-            const float4 b = *reinterpret_cast<const float4 *>(vec + kBN + 4 * q);
+            const float4 b = *reinterpret_cast<const float4 *>(vec + 128 + 4 * q);
             v[4 * q] += b.x, v[4 * q + 1] += b.y, v[4 * q + 2] += b.z, v[4 * q + 3] += b.w;
         }
     }
@@ -114,13 +121,18 @@ __device__ __forceinline__ uint4 finish(const uint32_t *acc, float xs, const flo
                       tc::pack_bf16(v[6 % kCols], v[7 % kCols]));
 }
 
-// The staging tiles of a pair's CTA in the order it fills them: column chunks of its tiles.
+// Column chunks (staging tiles) of tile t
+template <int OUT_COLS> __device__ __forceinline__ int chunks_of(int t, const Geo &geo)
+{
+    return (min(geo.bn, geo.N - tile_at(t, geo).n) + OUT_COLS - 1) / OUT_COLS;
+}
+
+// The chunks that one epilogue group of a pair's CTA takes, in order: g, g + 2, .. of each tile.
 template <int OUT_COLS> struct Chunks {
     int t, c;  // tile, column chunk
-    __device__ __forceinline__ void next(const Geo &geo, int step)
+    __device__ __forceinline__ void settle(const Geo &geo, int g, int step)
     {
-        const int n0 = tile_at(t, geo).n;
-        if (++c == kBN / OUT_COLS || n0 + OUT_COLS * c >= geo.N) c = 0, t += step;
+        while (t < geo.tiles && c >= chunks_of<OUT_COLS>(t, geo)) c = g, t += step;
     }
 };
 
@@ -131,9 +143,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                      const __grid_constant__ Geo geo, int *err)
 {
     constexpr int kOutCols = F32 ? 32 : 64;  // columns of a staging tile
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t raw = tc::smem_u32(smem_raw);
-    uint8_t *base = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t base[];
+    if (tc::smem_u32(base) & 1023u) {  // the swizzled tiles need it; the same for every thread of both CTAs
+        if (threadIdx.x == 0) atomicExch(err, MATE_ERR_INVALID_ARG);
+        return;
+    }
     uint64_t *bars = reinterpret_cast<uint64_t *>(base + kOffBar);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base + kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(base + kOffMisc + 4);
@@ -148,9 +162,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(&bars[kBarAccFull + i], 1);
-            tc::mbar_init(&bars[kBarAccEmpty + i], 8);  // the epilogue warps of both CTAs
+            tc::mbar_init(&bars[kBarAccEmpty + i], 2 * 4 * kGroups);  // the epilogue warps of both CTAs
         }
-        for (int i = 0; i < kSlots; ++i) tc::mbar_init(&bars[kBarAdd + i], 1);
+        for (int i = 0; i < kGroups * kSlots; ++i) tc::mbar_init(&bars[kBarAdd + i], 1);
         tc::mbar_init(&bars[kBarDrain], 1);
         tc::fence_mbar_init();
         *abort_flag = 0;
@@ -168,7 +182,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t it = 0;  // stage fills issued
             for (int t = pair; t < geo.tiles && !*abort_flag; t += pairs) {
                 const Tile at = tile_at(t, geo);
-                const int m0 = at.m + rank * 128, n0 = at.n + rank * 128;
+                const int m0 = at.m + rank * 128, n0 = at.n + rank * (geo.bn / 2);
                 for (int ks = 0; ks < geo.nk; ++ks, ++it) {
                     const int s = it % kStages;
                     const uint32_t round = it / kStages;
@@ -177,7 +191,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     uint8_t *sa = base + kOffStages + s * kStage, *sb = sa + kTile;
                     // both CTAs' four copies complete on rank 0's barrier
                     const uint32_t full = tc::cluster_addr(&bars[kBarFull + s], 0);
-                    if (rank == 0) tc::mbar_expect_tx(&bars[kBarFull + s], 2 * kStage);
+                    if (rank == 0) tc::mbar_expect_tx(&bars[kBarFull + s], 2 * kTile + geo.bn * kBK);
                     tc::tma_load_2d_pair(sa, &ma, full, ks * kBK, m0);
                     tc::tma_load_2d_pair(sb, &mb, full, ks * kBK, n0);
                 }
@@ -191,14 +205,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         // ---------------- MMA issue ----------------
         if (lane == 0 && rank == 0) {
-            const uint32_t idesc = tc::idesc_i8(kBM, kBN);
+            const uint32_t idesc = tc::idesc_i8(kBM, geo.bn);
             uint32_t it = 0, tl = 0, committed = 0;
             for (int t = pair; t < geo.tiles && !*abort_flag; t += pairs, ++tl) {
                 const uint32_t acc = tl & 1, use = tl >> 1;
                 if (use > 0 && !tc::mbar_wait_or_abort(&bars[kBarAccEmpty + acc], (use - 1) & 1u, err, abort_flag))
                     break;
                 tc::tc_fence_after();
-                const uint32_t d = tmem + acc * kBN;
+                const uint32_t d = tmem + acc * kMaxBN;
                 bool ok = true;
                 for (int ks = 0; ks < geo.nk; ++ks, ++it) {
                     const int s = it % kStages;
@@ -225,83 +239,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
         }
     } else {
-        // ---------------- epilogue: warps 2-5, TMEM lanes 32 (warp % 4) .. ----------------
-        const int et = tid - 64;                        // 0..127
+        // ---------------- epilogue: warps 2-9 in two groups, TMEM lanes 32 (warp % 4) .. ----------------
+        const int g = (tid - 64) / 128, et = (tid - 64) % 128;  // group, thread of it
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32);
-        const int row = (int)lane_base + lane;          // output row of the CTA's half tile
-        uint32_t tl = 0, chunks = 0;                    // tiles and staging tiles done
-        Chunks<kOutCols> ahead{pair, 0};                // the next addend chunk to ask for
+        const int row = (int)lane_base + lane;                  // output row of the CTA's half tile
+        uint8_t *slots = base + kOffOut + g * kSlots * kOutTile;
+        uint64_t *add = bars + kBarAdd + g * kSlots;
+        uint32_t tl = 0, done = 0;                              // tiles and staging tiles done
+        Chunks<kOutCols> ahead{pair, g};                        // the next addend chunk to ask for
         uint32_t asked = 0;
         auto ask = [&] {  // one thread: the addend of the next chunk into its slot
+            ahead.settle(geo, g, pairs);
             if (ahead.t >= geo.tiles) return;
             const uint32_t slot = asked % kSlots;
-            tc::mbar_expect_tx(&bars[kBarAdd + slot], kOutTile);
             const Tile at = tile_at(ahead.t, geo);
-            tc::tma_load_2d(base + kOffOut + slot * kOutTile, &md, &bars[kBarAdd + slot], at.n + kOutCols * ahead.c,
-                            at.m + rank * 128);
+            tc::mbar_expect_tx(&add[slot], kOutTile);
+            tc::tma_load_2d(slots + slot * kOutTile, &md, &add[slot], at.n + kOutCols * ahead.c, at.m + rank * 128);
             ++asked;
-            ahead.next(geo, pairs);
+            ahead.c += kGroups;
         };
-        if (geo.has_addend && et == 0) ask(), ask();
-        // the scales and biases of a tile's columns et and et + 128
-        float *vec = reinterpret_cast<float *>(base + kOffVec);
-        float ws[2], bs[2];
+        if (geo.has_addend && et == 0) ask();
+        // the scale and bias of the group's column et of a tile: column et % kOutCols of its chunk et / kOutCols
+        float *vec = reinterpret_cast<float *>(base + kOffVec) + g * 256;
+        const int own = (et / kOutCols * kGroups + g) * kOutCols + et % kOutCols;
+        float ws, bs;
         auto fetch = [&](int t) {
-            const int n = t < geo.tiles ? tile_at(t, geo).n + et : geo.N;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                ws[h] = n + 128 * h < geo.N ? geo.w_scale[n + 128 * h] : 0.f;
-                bs[h] = geo.bias && n + 128 * h < geo.N ? geo.bias[n + 128 * h] : 0.f;
-            }
+            const int n = t < geo.tiles ? tile_at(t, geo).n + own : geo.N;
+            ws = n < geo.N ? geo.w_scale[n] : 0.f;
+            bs = geo.bias && n < geo.N ? geo.bias[n] : 0.f;
         };
         fetch(pair);
         bool ok = true;
         for (int t = pair; t < geo.tiles && ok; t += pairs, ++tl) {
             const uint32_t acc = tl & 1, use = tl >> 1;
             // the last tile's readers passed the barrier of its last chunk
-#pragma unroll
-            for (int h = 0; h < 2; ++h) vec[et + 128 * h] = ws[h], vec[kBN + et + 128 * h] = bs[h];
+            vec[et] = ws, vec[128 + et] = bs;
             fetch(t + pairs);
-            if (!tc::named_all(1, 128, tc::mbar_wait_sleep(&bars[kBarAccFull + acc], use & 1u, err, abort_flag))) break;
+            if (!tc::named_all(1 + g, 128, tc::mbar_wait_sleep(&bars[kBarAccFull + acc], use & 1u, err, abort_flag))) break;
             tc::tc_fence_after();
             const Tile at = tile_at(t, geo);
-            const int m0 = at.m + rank * 128, n0 = at.n;
+            const int m0 = at.m + rank * 128, chunks = chunks_of<kOutCols>(t, geo);
             const float xs = m0 + row < geo.M ? geo.x_scale[m0 + row] : 0.f;
-            for (int c = 0; c < kBN / kOutCols && n0 + kOutCols * c < geo.N; ++c, ++chunks) {
-                const uint32_t slot = chunks % kSlots;
+            for (int c = g; c < chunks; c += kGroups, ++done) {
+                const uint32_t slot = done % kSlots;
+                const int n0 = at.n + kOutCols * c;
                 uint32_t v[kOutCols / 32][32];
 #pragma unroll
                 for (int q = 0; q < kOutCols / 32; ++q)
-                    tc::tmem_ld32u(tc::tmem_addr(tmem + acc * kBN, lane_base, kOutCols * c + 32 * q), v[q]);
+                    tc::tmem_ld32u(tc::tmem_addr(tmem + acc * kMaxBN, lane_base, kOutCols * c + 32 * q), v[q]);
                 tc::tmem_wait_ld();
                 if (geo.has_addend) {
-                    // asked for after the store that read this slot was done with it
-                    ok = tc::named_all(1, 128, tc::mbar_wait_or_abort(&bars[kBarAdd + slot], (chunks / kSlots) & 1u, err,
-                                                                      abort_flag));
+                    if (et == 0) {
+                        tc::bulk_wait_read<0>();  // the other slot is free again: the next chunk's addend
+                        ask();
+                    }
+                    ok = tc::named_all(1 + g, 128, tc::mbar_wait_or_abort(&add[slot], (done / kSlots) & 1u, err, abort_flag));
                     if (!ok) break;
                 } else {
                     if (et == 0) tc::bulk_wait_read<kSlots - 1>();
-                    tc::named_sync(1, 128);
+                    tc::named_sync(1 + g, 128);
                 }
-                uint8_t *stg = base + kOffOut + slot * kOutTile;
+                uint8_t *stg = slots + slot * kOutTile;
+                const float *cv = vec + c / kGroups * kOutCols;
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
-                    const int n = n0 + kOutCols * c + q * (kOutCols / 8);
-                    uint4 *at = reinterpret_cast<uint4 *>(stg + tc::sw128(row, q));
-                    // N is a multiple of 8: a 16-byte chunk is inside or outside as a whole
-                    if (n < geo.N)
-                        *at = finish<F32>(&v[q * (kOutCols / 8) / 32][q * (kOutCols / 8) % 32], xs, vec + (n - n0), geo, at);
+                    uint4 *to = reinterpret_cast<uint4 *>(stg + tc::sw128(row, q));
+                    // columns past N hold zeros and are not written
+                    *to = finish<F32>(&v[q * (kOutCols / 8) / 32][q * (kOutCols / 8) % 32], xs, cv + q * (kOutCols / 8), geo, to);
                 }
                 tc::fence_proxy_async_smem();
-                tc::named_sync(1, 128);
+                tc::named_sync(1 + g, 128);
                 if (et == 0) {
                     // rows past M and columns past N fall outside the tensor and are not written
-                    if (m0 < geo.M) tc::tma_store_2d(&mo, stg, n0 + kOutCols * c, m0);
+                    if (m0 < geo.M) tc::tma_store_2d(&mo, stg, n0, m0);
                     tc::bulk_commit();
-                    if (geo.has_addend) {
-                        tc::bulk_wait_read<kSlots - 2>();  // the slot two chunks on is free again
-                        ask();
-                    }
                 }
             }
             // this accumulator may be overwritten by the tile after next
@@ -311,8 +322,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (et == 0) {
             // the addends asked for have landed (bounded), the stores have completed
-            for (uint32_t i = chunks; i < asked; ++i)
-                tc::mbar_wait(&bars[kBarAdd + i % kSlots], (i / kSlots) & 1u, nullptr);
+            for (uint32_t i = done; i < asked; ++i) tc::mbar_wait(&add[i % kSlots], (i / kSlots) & 1u, nullptr);
             tc::bulk_wait_all();
         }
     }
@@ -326,6 +336,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
+// Columns of a tile: the width whose waves of tiles over the pairs cost least, a tile
+// costing its width and 32 columns more (its fixed costs, and the narrower tile's larger
+// share of loads).
+int tile_width(int64_t tiles_m, int n, int pairs)
+{
+    int best = 0;
+    int64_t least = 0;
+    for (int bn = kMaxBN; bn >= 128; bn -= 64) {
+        const int64_t waves = (tiles_m * ((n + bn - 1) / bn) + pairs - 1) / pairs;
+        if (!best || waves * (bn + 32) < least) best = bn, least = waves * (bn + 32);
+    }
+    return best;
+}
+
 }  // namespace
 
 // Rows of codes are 16-byte aligned (K a multiple of 16) and so are rows of outputs;
@@ -333,7 +357,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 bool linear_i8_supported(const LinearI8Args &a)
 {
     return a.M > 0 && a.N > 0 && a.K > 0 && a.K % 16 == 0 && a.K <= kMaxK && a.N % 8 == 0 &&
-           ((int64_t)a.M + kBM) * ((int64_t)a.N + kBN) / (kBM * kBN) < ((int64_t)1 << 30);
+           ((int64_t)a.M + kBM) * ((int64_t)a.N + 128) / (kBM * 128) < ((int64_t)1 << 30);
 }
 
 cudaError_t launch_linear_i8(const LinearI8Args &a, cudaStream_t s)
@@ -347,22 +371,25 @@ cudaError_t launch_linear_i8(const LinearI8Args &a, cudaStream_t s)
     if (e != cudaSuccess) return e;
     const TmapType ot = a.out_f32 ? TmapType::f32 : TmapType::bf16;
     const int oc = a.out_f32 ? 32 : 64;
+    const int64_t tiles_m = ((int64_t)a.M + kBM - 1) / kBM;
+    const int pairs = std::max(nsm / 2, 1), bn = tile_width(tiles_m, a.N, pairs);
     CUtensorMap ma, mb, mo, md;
-    if (!tmap_2d(&ma, TmapType::u8, a.x, a.K, a.M, kBK, 128) || !tmap_2d(&mb, TmapType::u8, a.w, a.K, a.N, kBK, 128) ||
+    if (!tmap_2d(&ma, TmapType::u8, a.x, a.K, a.M, kBK, 128) || !tmap_2d(&mb, TmapType::u8, a.w, a.K, a.N, kBK, bn / 2) ||
         !tmap_2d(&mo, ot, a.out, a.N, a.M, oc, 128) || !tmap_2d(&md, ot, a.addend ? a.addend : a.out, a.N, a.M, oc, 128))
         return cudaErrorInvalidValue;
     Geo geo;
     geo.M = a.M;
     geo.N = a.N;
     geo.nk = (a.K + kBK - 1) / kBK;
-    geo.tiles_n = (a.N + kBN - 1) / kBN;
-    geo.tiles_m = (int)(((int64_t)a.M + kBM - 1) / kBM);
+    geo.bn = bn;
+    geo.tiles_n = (a.N + bn - 1) / bn;
+    geo.tiles_m = (int)tiles_m;
     geo.tiles = geo.tiles_m * geo.tiles_n;
     geo.x_scale = a.x_scale;
     geo.w_scale = a.w_scale;
     geo.bias = a.bias;
     geo.has_addend = a.addend != nullptr;
-    const int grid = 2 * std::min(geo.tiles, std::max(nsm / 2, 1));
+    const int grid = 2 * std::min(geo.tiles, pairs);
     Phase ph(a.phase ? a.phase : MATE_PHASE_LINEAR_I8, s);
     kernel<<<grid, kThreads, kSmemBytes, s>>>(ma, mb, mo, md, geo, a.err);
     return cudaGetLastError();

@@ -135,19 +135,22 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int p = rank * pieces + tid; p < (rank + 1) * pieces; p += kThreads) {
         const int token = p / (kBC / 8), n = c0 + p % (kBC / 8) * 8, m = m0 + token;
         if (m >= geo.M || n >= geo.N) continue;  // N is a multiple of 8
-        int4 a = make_int4(0, 0, 0, 0), b = a;
         const int *at = part + token * kBC + p % (kBC / 8) * 8;
-        for (int r = 0; r < splits; ++r) {
-            int4 u, w;
-            if (splits > 1) {
-                const uint32_t addr = tc::cluster_addr(at, r);
-                u = tc::ld_cluster(addr), w = tc::ld_cluster(addr + 16);
-            } else {
-                u = *reinterpret_cast<const int4 *>(at), w = *reinterpret_cast<const int4 *>(at + 4);
+        int4 a = *reinterpret_cast<const int4 *>(at), b = *reinterpret_cast<const int4 *>(at + 4);
+        // the other CTAs' partial tiles, their loads all in flight at once
+        int4 u[7], w[7];
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            if (i < splits) {
+                const uint32_t addr = tc::cluster_addr(at, (rank + i) % splits);
+                u[i - 1] = tc::ld_cluster(addr), w[i - 1] = tc::ld_cluster(addr + 16);
             }
-            a.x += u.x, a.y += u.y, a.z += u.z, a.w += u.w;
-            b.x += w.x, b.y += w.y, b.z += w.z, b.w += w.w;
-        }
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            if (i < splits) {
+                a.x += u[i - 1].x, a.y += u[i - 1].y, a.z += u[i - 1].z, a.w += u[i - 1].w;
+                b.x += w[i - 1].x, b.y += w[i - 1].y, b.z += w[i - 1].z, b.w += w[i - 1].w;
+            }
         const float xs = geo.x_scale[m];
         const float4 wa = *reinterpret_cast<const float4 *>(geo.w_scale + n);
         const float4 wb = *reinterpret_cast<const float4 *>(geo.w_scale + n + 4);
