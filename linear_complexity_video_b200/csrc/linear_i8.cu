@@ -6,12 +6,11 @@
 // in fp32 in the epilogue, and the result is rounded once to the output type.
 //
 // Persistent CTA pairs (clusters of two, cta_group::2), 320 threads per CTA; a pair
-// computes output tiles of 256 x 256 (or 192 or 128 columns, tile_width), CTA r the
-// rows 128 r ..:
-//   warp 0    TMA loads of the CTA's 128 x 128 codes of x and its half of the w tile
-//             into a 5-stage ring (32 KB per stage and CTA, 128-byte swizzle,
-//             K-major; codes past K, M or N load as zeros), all completing on the
-//             barriers of rank 0;
+// computes output tiles of 256 x 256, CTA r the rows 128 r ..:
+//   warp 0    TMA loads of the CTA's 128 x 128 codes of x and its half, 128 x 128, of
+//             the w tile into a 5-stage ring (32 KB per stage and CTA, 128-byte
+//             swizzle, K-major; codes past K, M or N load as zeros), all completing on
+//             the barriers of rank 0;
 //   warp 1    TMEM allocation and, in rank 0, tcgen05.mma issue: four M = 256, N = 256,
 //             K = 32 MMAs per stage into one of two TMEM accumulators (2 x 256 columns
 //             in each CTA), so that a tile's epilogue runs while the next accumulates;
@@ -21,10 +20,20 @@
 //             store. The addend arrives in the staging tile by TMA, a chunk ahead; the
 //             columns' scales and bias wait in shared memory, fetched a tile ahead
 //             (read from global memory chunk by chunk they cost in_proj of 131,072
-//             tokens 3.20 ms instead of 2.48).
-// A pair reads 64 KB for the work that two single CTAs would read 96 KB for: the pair
-// halves each CTA's share of w. Tiles are walked in groups of eight tile rows, so that the
-// 74 pairs at work read about eight rows' x and nine columns' w.
+//             tokens 3.20 ms instead of 2.48). One group instead of two: 15.4 us
+//             instead of 12.8 for 1,155 tokens, 2,560 -> 2,560.
+// What bounds it: with its operands in place an MMA takes about 146 cycles (128 nominal,
+// and as long at N = 192 or 128, so a narrower tile gains nothing: 4,096 tokens, 2,560 ->
+// 2,560, take 30 us in 256 columns and 39 in 128); a K step of four takes 0.30 us, 0.33 with
+// its loads, and 0.37 to 0.39 in runs of a few hundred microseconds and more, where the
+// board's power limit lowers the clocks (2,450 to 2,800 TOP/s, 0.9 to 1.0 of twice the sustained
+// bf16 rate; 2,890 to 3,300 in single cold launches). Tried and left: a ring of six stages (no
+// change); tiles of 256 x 512 with x loaded once for both halves (a quarter less to load: 476 us
+// against 492 for 32,768 tokens, 7,680 -> 2,560, but 181 against 175 at K = 2,560, since one tile
+// fills TMEM and its epilogue is exposed).
+// Tiles are walked in groups of eight tile rows, so that the 74 pairs at work read about
+// eight rows' x and nine columns' w from L2 (in_proj of 131,072 tokens: 3.30 ms row by row,
+// 3.20 in groups).
 //
 // Every wait is bounded (2 s); a wait that gives up records MATE_ERR_TIMEOUT and
 // raises a CTA abort flag that makes every role leave its loop; the CTA then
@@ -42,7 +51,7 @@ namespace mate {
 namespace {
 
 constexpr int kBM = 256, kBK = 128;                  // rows of a pair's tile; a K step is 128 codes = one swizzled row
-constexpr int kMaxBN = 256;                          // columns of a tile, at most
+constexpr int kBN = 256;                             // columns of a tile
 constexpr int kStages = 5, kGroups = 2, kSlots = 2;  // staging tiles per epilogue group
 constexpr int kGroup = 8;                            // tile rows walked together
 constexpr uint32_t kTile = 128 * kBK;                // 16 KB: one CTA's part of x or w
@@ -51,7 +60,7 @@ constexpr uint32_t kOutTile = 128 * 128;             // 16 KB: 128 rows x 128 by
 constexpr uint32_t kOffStages = 0;
 constexpr uint32_t kOffOut = kStages * kStage;
 constexpr uint32_t kOffVec = kOffOut + kGroups * kSlots * kOutTile;  // per group: w_scale and bias of its columns
-constexpr uint32_t kOffBar = kOffVec + 2 * kMaxBN * 4;
+constexpr uint32_t kOffBar = kOffVec + 2 * kBN * 4;
 // full, empty (per stage), acc_full[2], acc_empty[2], addend (per slot), drain; then the TMEM slot and the abort flag
 constexpr int kBarFull = 0, kBarEmpty = kStages, kBarAccFull = 2 * kStages, kBarAccEmpty = 2 * kStages + 2,
               kBarAdd = 2 * kStages + 4, kBarDrain = kBarAdd + kGroups * kSlots, kNumBars = kBarDrain + 1;
@@ -65,7 +74,6 @@ static_assert(kOffBar % 8 == 0 && kOffVec % 16 == 0, "linear_i8: alignment");
 
 struct Geo {
     int M, N, nk;        // rows, columns, 128-wide K steps
-    int bn;              // columns of a tile: 256, 192 or 128
     int tiles_m, tiles_n, tiles;  // output tiles along M, along N, in total
     const float *x_scale, *w_scale, *bias;
     int has_addend;
@@ -80,7 +88,7 @@ __device__ __forceinline__ Tile tile_at(int t, const Geo &geo)
 {
     const int g = t / (kGroup * geo.tiles_n), r = t - g * kGroup * geo.tiles_n;
     const int rows = min(kGroup, geo.tiles_m - g * kGroup);
-    return {(g * kGroup + r % rows) * kBM, (r / rows) * geo.bn};
+    return {(g * kGroup + r % rows) * kBM, (r / rows) * kBN};
 }
 
 // eight (bf16) or four (fp32) outputs, one 16-byte chunk of a staging tile: `acc` scaled, plus
@@ -124,7 +132,7 @@ __device__ __forceinline__ uint4 finish(const uint32_t *acc, float xs, const flo
 // Column chunks (staging tiles) of tile t
 template <int OUT_COLS> __device__ __forceinline__ int chunks_of(int t, const Geo &geo)
 {
-    return (min(geo.bn, geo.N - tile_at(t, geo).n) + OUT_COLS - 1) / OUT_COLS;
+    return (min(kBN, geo.N - tile_at(t, geo).n) + OUT_COLS - 1) / OUT_COLS;
 }
 
 // The chunks that one epilogue group of a pair's CTA takes, in order: g, g + 2, .. of each tile.
@@ -182,7 +190,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             uint32_t it = 0;  // stage fills issued
             for (int t = pair; t < geo.tiles && !*abort_flag; t += pairs) {
                 const Tile at = tile_at(t, geo);
-                const int m0 = at.m + rank * 128, n0 = at.n + rank * (geo.bn / 2);
+                const int m0 = at.m + rank * 128, n0 = at.n + rank * 128;
                 for (int ks = 0; ks < geo.nk; ++ks, ++it) {
                     const int s = it % kStages;
                     const uint32_t round = it / kStages;
@@ -191,7 +199,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     uint8_t *sa = base + kOffStages + s * kStage, *sb = sa + kTile;
                     // both CTAs' four copies complete on rank 0's barrier
                     const uint32_t full = tc::cluster_addr(&bars[kBarFull + s], 0);
-                    if (rank == 0) tc::mbar_expect_tx(&bars[kBarFull + s], 2 * kTile + geo.bn * kBK);
+                    if (rank == 0) tc::mbar_expect_tx(&bars[kBarFull + s], 2 * kStage);
                     tc::tma_load_2d_pair(sa, &ma, full, ks * kBK, m0);
                     tc::tma_load_2d_pair(sb, &mb, full, ks * kBK, n0);
                 }
@@ -205,14 +213,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         // ---------------- MMA issue ----------------
         if (lane == 0 && rank == 0) {
-            const uint32_t idesc = tc::idesc_i8(kBM, geo.bn);
+            const uint32_t idesc = tc::idesc_i8(kBM, kBN);
             uint32_t it = 0, tl = 0, committed = 0;
             for (int t = pair; t < geo.tiles && !*abort_flag; t += pairs, ++tl) {
                 const uint32_t acc = tl & 1, use = tl >> 1;
                 if (use > 0 && !tc::mbar_wait_or_abort(&bars[kBarAccEmpty + acc], (use - 1) & 1u, err, abort_flag))
                     break;
                 tc::tc_fence_after();
-                const uint32_t d = tmem + acc * kMaxBN;
+                const uint32_t d = tmem + acc * kBN;
                 bool ok = true;
                 for (int ks = 0; ks < geo.nk; ++ks, ++it) {
                     const int s = it % kStages;
@@ -280,14 +288,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const Tile at = tile_at(t, geo);
             const int m0 = at.m + rank * 128, chunks = chunks_of<kOutCols>(t, geo);
             const float xs = m0 + row < geo.M ? geo.x_scale[m0 + row] : 0.f;
+            // the accumulator goes back to the MMAs (of the tile after next) once this group has its
+            // last chunk of it in registers
+            auto release = [&] {
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_cluster(tc::cluster_addr(&bars[kBarAccEmpty + acc], 0));
+            };
+            if (g >= chunks) release();
             for (int c = g; c < chunks; c += kGroups, ++done) {
                 const uint32_t slot = done % kSlots;
                 const int n0 = at.n + kOutCols * c;
                 uint32_t v[kOutCols / 32][32];
 #pragma unroll
                 for (int q = 0; q < kOutCols / 32; ++q)
-                    tc::tmem_ld32u(tc::tmem_addr(tmem + acc * kMaxBN, lane_base, kOutCols * c + 32 * q), v[q]);
+                    tc::tmem_ld32u(tc::tmem_addr(tmem + acc * kBN, lane_base, kOutCols * c + 32 * q), v[q]);
                 tc::tmem_wait_ld();
+                if (c + kGroups >= chunks) release();
                 if (geo.has_addend) {
                     if (et == 0) {
                         tc::bulk_wait_read<0>();  // the other slot is free again: the next chunk's addend
@@ -315,10 +332,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tc::bulk_commit();
                 }
             }
-            // this accumulator may be overwritten by the tile after next
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive_cluster(tc::cluster_addr(&bars[kBarAccEmpty + acc], 0));
         }
         if (et == 0) {
             // the addends asked for have landed (bounded), the stores have completed
@@ -336,20 +349,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
 }
 
-// Columns of a tile: the width whose waves of tiles over the pairs cost least, a tile
-// costing its width and 32 columns more (its fixed costs, and the narrower tile's larger
-// share of loads).
-int tile_width(int64_t tiles_m, int n, int pairs)
-{
-    int best = 0;
-    int64_t least = 0;
-    for (int bn = kMaxBN; bn >= 128; bn -= 64) {
-        const int64_t waves = (tiles_m * ((n + bn - 1) / bn) + pairs - 1) / pairs;
-        if (!best || waves * (bn + 32) < least) best = bn, least = waves * (bn + 32);
-    }
-    return best;
-}
-
 }  // namespace
 
 // Rows of codes are 16-byte aligned (K a multiple of 16) and so are rows of outputs;
@@ -357,7 +356,7 @@ int tile_width(int64_t tiles_m, int n, int pairs)
 bool linear_i8_supported(const LinearI8Args &a)
 {
     return a.M > 0 && a.N > 0 && a.K > 0 && a.K % 16 == 0 && a.K <= kMaxK && a.N % 8 == 0 &&
-           ((int64_t)a.M + kBM) * ((int64_t)a.N + 128) / (kBM * 128) < ((int64_t)1 << 30);
+           ((int64_t)a.M + kBM) * ((int64_t)a.N + kBN) / (kBM * kBN) < ((int64_t)1 << 30);
 }
 
 cudaError_t launch_linear_i8(const LinearI8Args &a, cudaStream_t s)
@@ -371,25 +370,22 @@ cudaError_t launch_linear_i8(const LinearI8Args &a, cudaStream_t s)
     if (e != cudaSuccess) return e;
     const TmapType ot = a.out_f32 ? TmapType::f32 : TmapType::bf16;
     const int oc = a.out_f32 ? 32 : 64;
-    const int64_t tiles_m = ((int64_t)a.M + kBM - 1) / kBM;
-    const int pairs = std::max(nsm / 2, 1), bn = tile_width(tiles_m, a.N, pairs);
     CUtensorMap ma, mb, mo, md;
-    if (!tmap_2d(&ma, TmapType::u8, a.x, a.K, a.M, kBK, 128) || !tmap_2d(&mb, TmapType::u8, a.w, a.K, a.N, kBK, bn / 2) ||
+    if (!tmap_2d(&ma, TmapType::u8, a.x, a.K, a.M, kBK, 128) || !tmap_2d(&mb, TmapType::u8, a.w, a.K, a.N, kBK, 128) ||
         !tmap_2d(&mo, ot, a.out, a.N, a.M, oc, 128) || !tmap_2d(&md, ot, a.addend ? a.addend : a.out, a.N, a.M, oc, 128))
         return cudaErrorInvalidValue;
     Geo geo;
     geo.M = a.M;
     geo.N = a.N;
     geo.nk = (a.K + kBK - 1) / kBK;
-    geo.bn = bn;
-    geo.tiles_n = (a.N + bn - 1) / bn;
-    geo.tiles_m = (int)tiles_m;
+    geo.tiles_n = (a.N + kBN - 1) / kBN;
+    geo.tiles_m = (int)(((int64_t)a.M + kBM - 1) / kBM);
     geo.tiles = geo.tiles_m * geo.tiles_n;
     geo.x_scale = a.x_scale;
     geo.w_scale = a.w_scale;
     geo.bias = a.bias;
     geo.has_addend = a.addend != nullptr;
-    const int grid = 2 * std::min(geo.tiles, pairs);
+    const int grid = 2 * std::min(geo.tiles, std::max(nsm / 2, 1));
     Phase ph(a.phase ? a.phase : MATE_PHASE_LINEAR_I8, s);
     kernel<<<grid, kThreads, kSmemBytes, s>>>(ma, mb, mo, md, geo, a.err);
     return cudaGetLastError();

@@ -112,7 +112,7 @@ SHAPES = [(1, 16, 8), (1, 2560, 7680), (2, 2560, 264), (7, 80, 40), (16, 2560, 2
           (33, 5120, 520), (64, 2560, 80), (65, 2560, 2560), (127, 272, 72), (128, 128, 256), (129, 2576, 264),
           (200, 7680, 136), (255, 400, 2560), (257, 128, 512), (300, 2560, 2560), (513, 1040, 776), (1155, 2560, 2560),
           (1155, 48, 10448), (2500, 5120, 264), (4097, 64, 64),
-          # the pairs' kernel at each of its tile widths, ragged in every direction
+          # the pairs' kernel, ragged in every direction, with one to eleven tile columns
           (1921, 144, 2312), (4225, 272, 2568), (9000, 400, 2504), (12800, 128, 1048), (513, 2576, 10440)]
 
 
