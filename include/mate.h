@@ -344,7 +344,7 @@ typedef struct {
  *   out     : (tokens, n) out_dtype, row-major, caller-owned; may be the addend
  *             itself (same address), otherwise overlaps no input
  * All pointers device memory; x_scale 4-byte aligned, the others 16-byte. k a multiple
- * of 16, k <= 131072; n a multiple of 8; tokens > 0. Results are bitwise
+ * of 16, k <= 131072; n a multiple of 8; tokens > 0, tokens and n at most 2^31 - 1024. Results are bitwise
  * reproducible. Returns MATE_OK, MATE_ERR_INVALID_ARG (bad pointers, sizes or
  * overlap), MATE_ERR_UNSUPPORTED (other dtype or sizes) or MATE_ERR_CUDA.
  */
@@ -376,7 +376,7 @@ typedef struct {
     int pre_norm;         /* MATE_NORM_RMS or MATE_NORM_LAYER: norm ahead of the next block */
     int x_dtype;          /* MATE_BF16 or MATE_F32: storage of x and x_out */
     int h_dtype;          /* MATE_BF16 or MATE_I8: storage of h */
-    int64_t mod_stride;   /* elements between batch elements in gate, scale and shift */
+    int64_t gate_stride, scale_stride, shift_stride; /* elements from one batch element's vector to the next's */
     float residual_scale; /* alpha */
     float eps;
 } mate_block_norm_dims;
@@ -395,8 +395,8 @@ typedef struct {
  *   x, x_out    : (batch, tokens, channels) x_dtype, row-major
  *   y           : (batch, tokens, channels) bf16, row-major
  *   w_post, w_pre : (channels) fp32, or NULL (ones)
- *   gate, scale, shift : channels fp32 per batch element, mod_stride elements
- *                 from one batch element's to the next's (0: all the same), or
+ *   gate, scale, shift : channels fp32 per batch element, each with its own
+ *                 stride between batch elements (0: one vector for all), or
  *                 NULL (gate 1, scale 0, shift 0)
  *   h           : (batch, tokens, channels) bf16 or int8, row-major
  *   h_scale     : (batch, tokens) fp32, with int8 h only (codes as above)
@@ -405,9 +405,11 @@ typedef struct {
  * outputs overlap neither an input nor one another. All pointers device memory;
  * x, y, x_out and h 16-byte aligned, fp32 vectors 4-byte aligned. channels a
  * multiple of 8, at most 8192; batch * tokens at most 2^30; eps >= 0 and finite;
- * residual_scale finite; mod_stride >= 0. Returns MATE_OK, MATE_ERR_INVALID_ARG (bad pointers, sizes,
- * eps, combinations or overlap), MATE_ERR_UNSUPPORTED (other dtypes, norms or
- * sizes) or MATE_ERR_CUDA.
+ * residual_scale finite; strides >= 0. Squares are summed in fp32, so magnitudes
+ * above about 1e18 overflow them. Results are bitwise reproducible. Returns
+ * MATE_OK, MATE_ERR_INVALID_ARG (bad pointers, sizes, eps, strides, combinations
+ * or overlap), MATE_ERR_UNSUPPORTED (other dtypes, norms or sizes) or
+ * MATE_ERR_CUDA.
  */
 int mate_block_norm_fwd(const void *x, const void *y, const float *w_post, const float *gate, const float *w_pre,
                         const float *scale, const float *shift, void *x_out, void *h, float *h_scale,

@@ -95,8 +95,8 @@ class mate_linear_i8_dims(ctypes.Structure):
 class mate_block_norm_dims(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int), ("tokens", ctypes.c_int), ("channels", ctypes.c_int),
                 ("post_norm", ctypes.c_int), ("pre_norm", ctypes.c_int), ("x_dtype", ctypes.c_int),
-                ("h_dtype", ctypes.c_int), ("mod_stride", ctypes.c_int64), ("residual_scale", ctypes.c_float),
-                ("eps", ctypes.c_float)]
+                ("h_dtype", ctypes.c_int), ("gate_stride", ctypes.c_int64), ("scale_stride", ctypes.c_int64),
+                ("shift_stride", ctypes.c_int64), ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
 class MateError(RuntimeError):

@@ -418,18 +418,16 @@ def block_norm(x, y=None, *, w_post=None, gate=None, residual_scale: float = 1.0
             _require(t, n, torch.float32)
             if t.shape != (C,):
                 raise ValueError(f"{n} must have one entry per channel")
-    mod_stride = None
+    strides = []
     for t, n in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
         if t is None:
+            strides.append(0)
             continue
         if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32:
             raise ValueError(f"{n} must be a float32 CUDA tensor")
         if t.shape not in ((batch, C), (C,)) or (C > 1 and t.stride(-1) != 1):
             raise ValueError(f"{n} must be (batch, C) or (C,), its channels contiguous")
-        s = 0 if t.dim() == 1 or batch == 1 else t.stride(0)
-        if mod_stride not in (None, s):
-            raise ValueError("gate, scale and shift must have one stride between batch elements")
-        mod_stride = s
+        strides.append(0 if t.dim() == 1 or batch == 1 else t.stride(0))
     _same_device(x, y, w_post, gate, w_pre, scale, shift)
     if _elsewhere(x, stream):
         with _on(x, stream):
@@ -444,7 +442,7 @@ def block_norm(x, y=None, *, w_post=None, gate=None, residual_scale: float = 1.0
             h_scale = x.new_empty(x.shape[:-1], dtype=torch.float32)
     kind = _NORMS[norm]
     dims = mate_block_norm_dims(batch, _rows(inner), C, kind if post_norm else MATE_NORM_NONE, kind, _DT[x.dtype],
-                                MATE_I8 if h_scale is not None else MATE_BF16, mod_stride or 0, residual_scale, eps)
+                                MATE_I8 if h_scale is not None else MATE_BF16, *strides, residual_scale, eps)
     mate_block_norm_fwd(x, y, w_post, gate, w_pre, scale, shift, x_out, h, h_scale, dims, _current(x))
     return x_out, (Codes(h, h_scale) if h_scale is not None else h)
 

@@ -135,14 +135,15 @@ __global__ void __launch_bounds__(TPR *ROWS, CTAS) block_norm_kernel(BlockNormAr
     };
     if (r0 + slot < r1) load(r0 + slot);
     {
-        const int64_t m = (int64_t)b * a.mod_stride;
+        const float *gate = a.gate + (int64_t)b * a.gate_stride, *scale = a.scale + (int64_t)b * a.scale_stride,
+                    *shift = a.shift + (int64_t)b * a.shift_stride;  // used where given
         float *g = reinterpret_cast<float *>(cg), *w = reinterpret_cast<float *>(ca), *s = reinterpret_cast<float *>(cs);
         for (int c = threadIdx.x; c < a.C; c += TPR * ROWS) {
             const int at = ((c >> 2 & 1) * nv + (c >> 3)) * 4 + (c & 3);
-            if (a.y) g[at] = (a.gate ? a.gate[m + c] : 1.f) * (a.w_post ? a.w_post[c] : 1.f);
+            if (a.y) g[at] = (a.gate ? gate[c] : 1.f) * (a.w_post ? a.w_post[c] : 1.f);
             if (a.h) {
-                w[at] = (a.w_pre ? a.w_pre[c] : 1.f) * (a.scale ? 1.f + a.scale[m + c] : 1.f);
-                s[at] = a.shift ? a.shift[m + c] : 0.f;
+                w[at] = (a.w_pre ? a.w_pre[c] : 1.f) * (a.scale ? 1.f + scale[c] : 1.f);
+                s[at] = a.shift ? shift[c] : 0.f;
             }
         }
     }

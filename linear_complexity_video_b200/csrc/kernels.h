@@ -155,14 +155,14 @@ struct LinearI8Args {
 // h = N(r) w_pre (1 + scale) + shift. Rows (batch, n), C channels.
 struct BlockNormArgs {
     const void *x, *y;       // (batch, n, C): fp32 or bf16; bf16
-    const float *w_post, *gate, *w_pre, *scale, *shift;  // (C); (batch, C) rows mod_stride apart
+    const float *w_post, *gate, *w_pre, *scale, *shift;  // (C); (batch, C) rows a stride apart
     void *x_out, *h;
     float *h_scale;
     int batch, n, C;
     int post, pre;           // MATE_NORM_*
     int x_f32;
     int h_type;              // MATE_BF16, MATE_F32 or MATE_I8
-    int64_t mod_stride;
+    int64_t gate_stride, scale_stride, shift_stride;
     float alpha, eps;
 };
 

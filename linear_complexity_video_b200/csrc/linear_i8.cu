@@ -355,7 +355,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 // output tiles fit 32-bit counters.
 bool linear_i8_supported(const LinearI8Args &a)
 {
-    return a.M > 0 && a.N > 0 && a.K > 0 && a.K % 16 == 0 && a.K <= kMaxK && a.N % 8 == 0 &&
+    constexpr int kMost = 0x7fffffff - 1023;  // a tile may reach past the last row or column
+    return a.M > 0 && a.N > 0 && a.M <= kMost && a.N <= kMost && a.K > 0 && a.K % 16 == 0 && a.K <= kMaxK && a.N % 8 == 0 &&
            ((int64_t)a.M + kBM) * ((int64_t)a.N + kBN) / (kBM * kBN) < ((int64_t)1 << 30);
 }
 

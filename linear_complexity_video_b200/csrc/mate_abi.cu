@@ -492,7 +492,7 @@ int mate_block_norm_fwd(const void *x, const void *y, const float *w_post, const
                         const mate_block_norm_dims *d, void *stream)
 {
     if (!d || d->batch <= 0 || d->tokens <= 0 || d->channels <= 0 || !(d->eps >= 0.f) || !isfinite(d->eps) ||
-        !isfinite(d->residual_scale) || d->mod_stride < 0)
+        !isfinite(d->residual_scale) || d->gate_stride < 0 || d->scale_stride < 0 || d->shift_stride < 0)
         return MATE_ERR_INVALID_ARG;
     if ((d->x_dtype != MATE_BF16 && d->x_dtype != MATE_F32) || d->post_norm < MATE_NORM_NONE ||
         d->post_norm > MATE_NORM_LAYER)
@@ -509,7 +509,9 @@ int mate_block_norm_fwd(const void *x, const void *y, const float *w_post, const
     a.pre = d->pre_norm;
     a.x_f32 = d->x_dtype == MATE_F32;
     a.h_type = d->h_dtype;
-    a.mod_stride = d->mod_stride;
+    a.gate_stride = d->gate_stride;
+    a.scale_stride = d->scale_stride;
+    a.shift_stride = d->shift_stride;
     a.alpha = d->residual_scale;
     a.eps = d->eps;
     if (!block_norm_supported(a)) return MATE_ERR_UNSUPPORTED;
@@ -524,14 +526,18 @@ int mate_block_norm_fwd(const void *x, const void *y, const float *w_post, const
     for (const void *p : vecs)
         if (!aligned(p, 4)) return MATE_ERR_INVALID_ARG;
     const size_t n = (size_t)a.batch * a.n * a.C, xb = n * (a.x_f32 ? 4 : 2), wb = (size_t)a.C * 4;
-    if ((uint64_t)a.mod_stride > ((uint64_t)1 << 40)) return MATE_ERR_UNSUPPORTED;
-    const size_t mb = ((size_t)(a.batch - 1) * (size_t)a.mod_stride + a.C) * 4;
+    const int64_t kMaxStride = (int64_t)1 << 30;  // spans stay far inside 64 bits
+    if (a.gate_stride > kMaxStride || a.scale_stride > kMaxStride || a.shift_stride > kMaxStride)
+        return MATE_ERR_UNSUPPORTED;
+    auto span = [&](const float *v, int64_t stride) {
+        return v ? ((size_t)(a.batch - 1) * (size_t)stride + a.C) * 4 : 0;
+    };
     const Range outs[3] = {{h, h ? n * (i8 ? 1 : 2) : 0},
                            {h_scale, i8 ? (size_t)a.batch * a.n * 4 : 0},
                            {x_out, x_out ? xb : 0}};
-    const Range ins[7] = {{y, y ? n * 2 : 0},       {w_post, w_post ? wb : 0}, {gate, gate ? mb : 0},
-                          {w_pre, w_pre ? wb : 0},  {scale, scale ? mb : 0},   {shift, shift ? mb : 0},
-                          {x, xb}};
+    const Range ins[7] = {{y, y ? n * 2 : 0},       {w_post, w_post ? wb : 0}, {gate, span(gate, a.gate_stride)},
+                          {w_pre, w_pre ? wb : 0},  {scale, span(scale, a.scale_stride)},
+                          {shift, span(shift, a.shift_stride)}, {x, xb}};
     // x_out may be x itself: each row is read whole before it is written
     if (!disjoint(outs, 2, ins, 7) || !disjoint(outs, 3, ins, x_out == x ? 6 : 7)) return MATE_ERR_INVALID_ARG;
     a.x = x;

@@ -51,7 +51,7 @@ def test_linear_i8_refusals():
     for d in ((0, 256, 64, BF16), (128, 0, 64, BF16), (128, 256, 0, BF16), (-5, 256, 64, BF16)):
         assert call(d) == INVALID, d
     for d in ((128, 256, 64, I8), (128, 250, 64, BF16), (128, 8, 64, BF16), (128, 256, 60, BF16),
-              (128, 131088, 64, BF16), (128, 256, 64, 9)):
+              (128, 131088, 64, BF16), (128, 256, 64, 9), (2**31 - 1, 256, 64, BF16), (128, 256, 2**31 - 8, BF16)):
         assert call(d) == UNSUPPORTED, d
     for n in ("x", "xs", "w", "ws", "out"):
         assert call(ok, **{n: None}) == INVALID, n
@@ -97,8 +97,8 @@ def test_block_norm_refusals():
     names = ("x", "y", "w_post", "gate", "w_pre", "scale", "shift", "x_out", "h", "h_scale")
 
     def dims(**kw):
-        a = dict(batch=2, tokens=8, channels=64, post_norm=1, pre_norm=1, x_dtype=BF16, h_dtype=BF16, mod_stride=192,
-                 residual_scale=1.0, eps=1e-6)
+        a = dict(batch=2, tokens=8, channels=64, post_norm=1, pre_norm=1, x_dtype=BF16, h_dtype=BF16, gate_stride=192,
+                 scale_stride=128, shift_stride=64, residual_scale=1.0, eps=1e-6)
         a.update(kw)
         return _lib.mate_block_norm_dims(*a.values())
 
@@ -111,11 +111,11 @@ def test_block_norm_refusals():
     assert call(None) == INVALID
     for kw in (dict(batch=0), dict(tokens=0), dict(channels=0), dict(channels=-8), dict(eps=-1.0),
                dict(eps=float("nan")), dict(eps=float("inf")), dict(residual_scale=float("nan")),
-               dict(residual_scale=float("inf")), dict(mod_stride=-1)):
+               dict(residual_scale=float("inf")), dict(gate_stride=-1), dict(scale_stride=-1), dict(shift_stride=-1)):
         assert call(dims(**kw)) == INVALID, kw
     for kw in (dict(channels=60), dict(channels=8200), dict(x_dtype=I8), dict(h_dtype=F32), dict(h_dtype=9),
                dict(post_norm=3), dict(post_norm=-1), dict(pre_norm=0), dict(pre_norm=3),
-               dict(batch=1 << 16, tokens=1 << 15), dict(mod_stride=1 << 41)):
+               dict(batch=1 << 16, tokens=1 << 15), dict(gate_stride=1 << 31), dict(shift_stride=1 << 62)):
         assert call(dims(**kw)) == UNSUPPORTED, kw
     # x is always there; y and x_out come together; something has to be asked for
     assert call(x=None) == INVALID and call(y=None) == INVALID and call(x_out=None) == INVALID
@@ -134,11 +134,11 @@ def test_block_norm_refusals():
     for n in ("w_post", "gate", "w_pre", "scale", "shift"):
         assert call(**{n: _p(names.index(n), 2)}) == INVALID, n
     assert call(dims(h_dtype=I8), h_scale=_p(9, 2)) == INVALID
-    # overlaps; the modulation's vectors reach over (batch - 1) strides
+    # overlaps; a modulation vector reaches over (batch - 1) strides of its own
     assert call(x_out=_p(0, 16)) == INVALID and call(x_out=_p(1)) == INVALID and call(h=_p(0)) == INVALID
     assert call(h=_p(7, 2 * 8 * 64 * 2 - 16)) == INVALID
-    for n in ("gate", "scale", "shift"):
-        assert call(h=_p(names.index(n), 192 * 4 + 64 * 4 - 16)) == INVALID, n
+    for n, stride in (("gate", 192), ("scale", 128), ("shift", 64)):
+        assert call(h=_p(names.index(n), stride * 4 + 64 * 4 - 16)) == INVALID, n
     assert call(dims(h_dtype=I8), h_scale=_p(0, 64)) == INVALID
     assert call(x_out=_p(0), h=_p(0, 512)) == INVALID  # in place, and h over both
 

@@ -101,6 +101,10 @@ def test_defaults_are_neutral_and_vectors_broadcast():
     for form in (one, {k: v.expand(3, -1) for k, v in one.items()}):
         got = mate.block_norm(d["x"], d["y"], **form)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # each vector with a stride of its own
+    got = mate.block_norm(d["x"], d["y"], gate=d["gate"][:1].expand(3, -1), scale=d["scale"].contiguous(), shift=one["shift"])
+    want = mate.block_norm(d["x"], d["y"], gate=one["gate"], scale=d["scale"], shift=one["shift"].repeat(3, 1))
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     # a modulation tensor whose columns start off a 16-byte boundary
     m = torch.randn(3, 3 * 264 + 1, device="cuda")
     a = mate.block_norm(d["x"], scale=m[:, 1:265])
