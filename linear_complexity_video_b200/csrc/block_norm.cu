@@ -87,6 +87,17 @@ __device__ __forceinline__ void load8(const float4 *plane, int nv, int v, float2
     f[0] = make_float2(a.x, a.y), f[1] = make_float2(a.z, a.w), f[2] = make_float2(b.x, b.y), f[3] = make_float2(b.z, b.w);
 }
 
+__device__ __forceinline__ float4 all4(float v) { return make_float4(v, v, v, v); }
+
+__device__ __forceinline__ float4 mul4(float4 a, float4 b) { return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w); }
+
+// four floats of a vector that may start at any of them
+__device__ __forceinline__ float4 load4(const float *p)
+{
+    if ((reinterpret_cast<uintptr_t>(p) & 15) == 0) return *reinterpret_cast<const float4 *>(p);
+    return make_float4(p[0], p[1], p[2], p[3]);
+}
+
 // TPR threads per row, up to VPL vectors of eight channels per thread. LAYER: one of the
 // norms is a layer norm (without, no mean is taken or subtracted). The arithmetic runs on
 // packed fp32 pairs: unpacked, the kernel was bound by its issue slots (66% issued, with
@@ -137,13 +148,15 @@ __global__ void __launch_bounds__(TPR *ROWS, CTAS) block_norm_kernel(BlockNormAr
     {
         const float *gate = a.gate + (int64_t)b * a.gate_stride, *scale = a.scale + (int64_t)b * a.scale_stride,
                     *shift = a.shift + (int64_t)b * a.shift_stride;  // used where given
-        float *g = reinterpret_cast<float *>(cg), *w = reinterpret_cast<float *>(ca), *s = reinterpret_cast<float *>(cs);
-        for (int c = threadIdx.x; c < a.C; c += TPR * ROWS) {
-            const int at = ((c >> 2 & 1) * nv + (c >> 3)) * 4 + (c & 3);
-            if (a.y) g[at] = (a.gate ? gate[c] : 1.f) * (a.w_post ? a.w_post[c] : 1.f);
+        // four channels at a time: half of a thread's eight, in one plane
+        for (int q = threadIdx.x; q < 2 * nv; q += TPR * ROWS) {
+            const int at = (q & 1) * nv + (q >> 1);
+            if (a.y) cg[at] = mul4(a.gate ? load4(gate + 4 * q) : all4(1.f), a.w_post ? load4(a.w_post + 4 * q) : all4(1.f));
             if (a.h) {
-                w[at] = (a.w_pre ? a.w_pre[c] : 1.f) * (a.scale ? 1.f + scale[c] : 1.f);
-                s[at] = a.shift ? shift[c] : 0.f;
+                const float4 s = a.scale ? load4(scale + 4 * q) : all4(0.f);
+                ca[at] = mul4(a.w_pre ? load4(a.w_pre + 4 * q) : all4(1.f),
+                              make_float4(1.f + s.x, 1.f + s.y, 1.f + s.z, 1.f + s.w));
+                cs[at] = a.shift ? load4(shift + 4 * q) : all4(0.f);
             }
         }
     }

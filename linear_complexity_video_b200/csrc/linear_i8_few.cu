@@ -5,7 +5,7 @@
 // The product is taken the other way round, out^T = w x^T: output channels are the MMA's
 // M = 128 rows and tokens its N = NT columns (16, 32 or 64), so that few tokens waste no
 // tensor time and w streams through at the rate of memory. The walk along K is split over
-// the CTAs of a cluster (1, 2, 4 or 8), each of which holds an exact int32 partial tile:
+// the CTAs of a cluster (1, 2 or 4), each of which holds an exact int32 partial tile:
 // they meet in shared memory, every CTA adding up its share of the tokens from the others'
 // (distributed shared memory; integer sums, so the split changes no bit of the result),
 // and finishing them (scales, bias, addend, one rounding) as it stores them.
@@ -138,15 +138,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int *at = part + token * kBC + p % (kBC / 8) * 8;
         int4 a = *reinterpret_cast<const int4 *>(at), b = *reinterpret_cast<const int4 *>(at + 4);
         // the other CTAs' partial tiles, their loads all in flight at once
-        int4 u[7], w[7];
+        int4 u[3], w[3];
 #pragma unroll
-        for (int i = 1; i < 8; ++i)
+        for (int i = 1; i < 4; ++i)
             if (i < splits) {
                 const uint32_t addr = tc::cluster_addr(at, (rank + i) % splits);
                 u[i - 1] = tc::ld_cluster(addr), w[i - 1] = tc::ld_cluster(addr + 16);
             }
 #pragma unroll
-        for (int i = 1; i < 8; ++i)
+        for (int i = 1; i < 4; ++i)
             if (i < splits) {
                 a.x += u[i - 1].x, a.y += u[i - 1].y, a.z += u[i - 1].z, a.w += u[i - 1].w;
                 b.x += w[i - 1].x, b.y += w[i - 1].y, b.z += w[i - 1].z, b.w += w[i - 1].w;
@@ -211,9 +211,11 @@ template <int NT> cudaError_t launch(const LinearI8Args &a, int nsm, cudaStream_
     geo.addend = a.addend;
     geo.out = a.out;
     const int64_t tiles = (int64_t)geo.tiles_n * ((a.M + NT - 1) / NT);
-    // as many CTAs as fit the GPU at two per SM
+    // as many CTAs as fit the GPU at two per SM, four to a tile at most: more spend longer on
+    // joining than they save (2,560 -> 2,560 in a graph, 1, 2, 4, 8 CTAs: 16 tokens 8.5, 6.7, 5.6,
+    // 6.1 us; 64 tokens 10.4, 8.5, 7.3, 9.0; 7,680 -> 2,560, 64 tokens 21, 14, 10, 11)
     int splits = 1;
-    while (splits < 8 && 2 * splits <= geo.nk && 2 * splits * tiles <= 2 * nsm) splits *= 2;
+    while (splits < 4 && 2 * splits <= geo.nk && 2 * splits * tiles <= 2 * nsm) splits *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * splits));
     cfg.blockDim = dim3(kThreads);
