@@ -9,7 +9,9 @@
  *     Scan orders, optionally preceded by review tokens;
  *   - the TE-branch: TEmporal Swin Attention (TESA), softmax attention inside
  *     fixed Tw x Sw x Sw windows whose placement is shifted on alternate
- *     layers.
+ *     layers;
+ * and, around them, the block's other parts (front-end, gated norm, composition),
+ * its matrix products in 8 bits, and the norms of a residual layer.
  * Sources: "LinGen: Towards High-Resolution Minute-Length Text-to-Video
  * Generation with Linear Computational Complexity" (xllm-io paper review),
  * section 三 "技术架构", MA-Branch items 1-3 and TE-Branch; the QbitAI news

@@ -695,7 +695,7 @@ const char *mate_status_string(int code)
     }
 }
 
-int mate_version(void) { return 100; }
+int mate_version(void) { return 200; }
 
 void mate_set_phase_hook(mate_phase_hook fn, void *user)
 {

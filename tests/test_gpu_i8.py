@@ -241,7 +241,7 @@ def _chain_inputs(M, seed):
     return x, y, z
 
 
-@pytest.mark.parametrize("M", [3, 400])
+@pytest.mark.parametrize("M", [3, 400, 20000])
 def test_captured_and_replayed(M):
     """One capture, replayed on new inputs: the results of the eager calls, bit for bit; the
     error word still reads clean."""
@@ -264,10 +264,11 @@ def test_captured_and_replayed(M):
     assert mate.mate_last_error() == 0
 
 
-def test_two_streams_at_once():
+@pytest.mark.parametrize("M", [700, 9001])
+def test_two_streams_at_once(M):
     w = mate.quantize_rows(torch.randn(520, 256, generator=_gen(1)).to(torch.bfloat16).cuda())
     wn = torch.ones(128, device="cuda")
-    ins = [_chain_inputs(700, s) for s in (5, 6)]
+    ins = [_chain_inputs(M, s) for s in (5, 6)]
     want = [_chain(i[0], w, i[1], i[2], wn) for i in ins]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in ins]
@@ -280,6 +281,29 @@ def test_two_streams_at_once():
     for k in range(2):
         for outs in got[k]:
             assert all(torch.equal(a, b) for a, b in zip(outs, want[k]))
+
+
+def test_two_graphs_of_one_workspace_free_chain():
+    """Two captured graphs of the same calls, replayed in turn and on two streams: nothing is shared."""
+    w = mate.quantize_rows(torch.randn(520, 256, generator=_gen(1)).to(torch.bfloat16).cuda())
+    wn = torch.ones(128, device="cuda")
+    ins = [_chain_inputs(m, s) for m, s in ((30, 7), (9001, 8))]
+    want = [_chain(i[0], w, i[1], i[2], wn) for i in ins]
+    torch.cuda.synchronize()
+    graphs = []
+    for i in ins:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs = _chain(i[0], w, i[1], i[2], wn)
+        graphs.append((g, outs))
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(4):
+        for (g, _o), st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+    torch.cuda.synchronize()
+    for (_g, outs), ref in zip(graphs, want):
+        assert all(torch.equal(a, b) for a, b in zip(outs, ref))
 
 
 @pytest.mark.parametrize("as_handle", [False, True])
