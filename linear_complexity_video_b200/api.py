@@ -521,7 +521,7 @@ def _block_i8(u, w, scan_mode, review_pool, chunk, nheads, headdim, ngroups, dst
     y_te = tesa(q, k, v, Tw, Sw, shift)
     c_te = quantize_rows(y_te.view(b, T, H, W, attn_heads * attn_dim))
     # the branches' codes have scales of their own: the second product adds the first, which is rounded to
-    # bf16 on the way (by at most 2^-8 of itself, half of what the codes leave it off by)
+    # bf16 on the way (by at most 2^-8 of itself; the codes leave it off by about 1%)
     te = linear_i8(*c_te, *w["w_te"])
     if keep:
         out = linear_i8(*y_ma, *w["w_ma"], addend=te)

@@ -163,7 +163,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)tc::cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
+    if (tid == 64) {
+        tc::tma_prefetch_map(&mo);
+        if (geo.has_addend) tc::tma_prefetch_map(&md);
+    }
     if (tid == 0) {
+        tc::tma_prefetch_map(&ma);
+        tc::tma_prefetch_map(&mb);
         for (int i = 0; i < kStages; ++i) {
             tc::mbar_init(&bars[kBarFull + i], 1);
             tc::mbar_init(&bars[kBarEmpty + i], 1);
@@ -283,11 +289,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             // the last tile's readers passed the barrier of its last chunk
             vec[et] = ws, vec[128 + et] = bs;
             fetch(t + pairs);
-            if (!tc::named_all(1 + g, 128, tc::mbar_wait_sleep(&bars[kBarAccFull + acc], use & 1u, err, abort_flag))) break;
-            tc::tc_fence_after();
             const Tile at = tile_at(t, geo);
             const int m0 = at.m + rank * 128, chunks = chunks_of<kOutCols>(t, geo);
             const float xs = m0 + row < geo.M ? geo.x_scale[m0 + row] : 0.f;
+            if (!tc::named_all(1 + g, 128, tc::mbar_wait_sleep(&bars[kBarAccFull + acc], use & 1u, err, abort_flag))) break;
+            tc::tc_fence_after();
             // the accumulator goes back to the MMAs (of the tile after next) once this group has its
             // last chunk of it in registers
             auto release = [&] {
