@@ -76,15 +76,9 @@ def _on(t: torch.Tensor, stream):
             yield stream
 
 
-def _elsewhere(t: torch.Tensor, stream) -> bool:
-    """Whether a call on `t` has to switch streams or devices (see _on); otherwise it runs on the
-    current stream as it stands, without the cost of the switch."""
-    return stream is not None or t.get_device() != torch.cuda.current_device()
-
-
-def _current(t: torch.Tensor) -> int:
-    """Handle of the current stream of `t`'s device, which is the current one."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
+def _current(dev: int) -> int:
+    """Handle of the current stream of device `dev`, without making a stream object."""
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _addr(t: Optional[torch.Tensor]):
@@ -313,23 +307,22 @@ def quantize_rows(x, stream=None) -> Codes:
     nn.Linear weight. Returns Codes(q (..., K) int8, scale (...) fp32) with
     scale = max|x| / 127 and q = rint(127 x / max|x|)."""
     _require(x, "x", torch.bfloat16)
-    if _elsewhere(x, stream):
-        with _on(x, stream):
-            return quantize_rows(x)
     if x.dim() < 1:
         raise ValueError("x must be (..., K)")
-    *lead, K = x.shape
-    q, scale = x.new_empty(x.shape, dtype=torch.int8), x.new_empty(lead, dtype=torch.float32)
-    mate_quant_rows_fwd(x, q, scale, mate_quant_dims(_rows(lead), K, MATE_BF16), _current(x))
+    dev = x.get_device()
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        with _on(x, stream):
+            return quantize_rows(x)
+    q, scale = torch.empty_like(x, dtype=torch.int8), x.new_empty(x.shape[:-1], dtype=torch.float32)
+    dims = mate_quant_dims(scale.numel(), x.shape[-1], MATE_BF16)
+    rc = _lib.load().mate_quant_rows_fwd(x.data_ptr(), q.data_ptr(), scale.data_ptr(), ctypes.byref(dims), _current(dev))
+    check("mate_quant_rows_fwd", rc)
     return Codes(q, scale)
 
 
-def linear_i8(x_q, x_scale, w_q, w_scale, bias=None, addend=None, out_dtype=torch.bfloat16,
-              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """8-bit linear layer: x_scale w_scale (x_q w_q^T) + bias + addend, the sum exact and one
-    rounding to out_dtype (bf16 or fp32). x_q: (..., K) int8; x_scale: (...) fp32; w_q: (N, K)
-    int8; w_scale: (N,) fp32; bias: (N,) fp32; addend: (..., N) out_dtype, and may be `out`.
-    Returns (..., N)."""
+def _check_linear_i8(x_q, x_scale, w_q, w_scale, bias, addend, out_dtype):
+    """Every argument check of linear_i8 with its message; linear_i8 itself asks the same in one
+    expression and comes here when it does not hold."""
     if out_dtype not in _DT:
         raise ValueError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
     _require(x_q, "x_q", torch.int8)
@@ -338,8 +331,7 @@ def linear_i8(x_q, x_scale, w_q, w_scale, bias=None, addend=None, out_dtype=torc
     _require(w_scale, "w_scale", torch.float32)
     if w_q.dim() != 2 or x_q.dim() < 1 or x_q.shape[-1] != w_q.shape[1]:
         raise ValueError("x_q must be (..., K) and w_q (N, K)")
-    N, K = w_q.shape
-    shape = x_scale.shape + (N,)
+    N = w_q.shape[0]
     if x_q.shape[:-1] != x_scale.shape or w_scale.shape != (N,):
         raise ValueError("x_scale must have one entry per token and w_scale one per row of w_q")
     if bias is not None:
@@ -348,15 +340,43 @@ def linear_i8(x_q, x_scale, w_q, w_scale, bias=None, addend=None, out_dtype=torc
             raise ValueError("bias must have one entry per row of w_q")
     if addend is not None:
         _require(addend, "addend", out_dtype)
-        if addend.shape != shape:
-            raise ValueError(f"addend must have shape {tuple(shape)}")
+        if addend.shape != x_scale.shape + (N,):
+            raise ValueError(f"addend must have shape {tuple(x_scale.shape) + (N,)}")
     _same_device(x_q, x_scale, w_q, w_scale, bias, addend)
-    if _elsewhere(x_q, stream):
+
+
+def linear_i8(x_q, x_scale, w_q, w_scale, bias=None, addend=None, out_dtype=torch.bfloat16,
+              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """8-bit linear layer: x_scale w_scale (x_q w_q^T) + bias + addend, the sum exact and one
+    rounding to out_dtype (bf16 or fp32). x_q: (..., K) int8; x_scale: (...) fp32; w_q: (N, K)
+    int8; w_scale: (N,) fp32; bias: (N,) fp32; addend: (..., N) out_dtype, and may be `out`.
+    Returns (..., N)."""
+    try:
+        dev, (N, K) = x_q.get_device(), w_q.shape
+        fine = (dev >= 0 and out_dtype in _DT
+                and x_q.dtype is torch.int8 and w_q.dtype is torch.int8
+                and x_scale.dtype is torch.float32 and w_scale.dtype is torch.float32
+                and w_q.get_device() == dev and x_scale.get_device() == dev and w_scale.get_device() == dev
+                and x_q.is_contiguous() and w_q.is_contiguous() and x_scale.is_contiguous() and w_scale.is_contiguous()
+                and x_q.shape == (*x_scale.shape, K) and w_scale.shape == (N,)
+                and (bias is None or (bias.dtype is torch.float32 and bias.get_device() == dev and bias.is_contiguous()
+                                      and bias.shape == (N,)))
+                and (addend is None or (addend.dtype is out_dtype and addend.get_device() == dev
+                                        and addend.is_contiguous() and addend.shape == (*x_scale.shape, N))))
+    except (AttributeError, TypeError, ValueError):
+        fine = False
+    if not fine:
+        _check_linear_i8(x_q, x_scale, w_q, w_scale, bias, addend, out_dtype)
+        dev, (N, K) = x_q.get_device(), w_q.shape
+    if stream is not None or dev != torch._C._cuda_getDevice():
         with _on(x_q, stream):
             return linear_i8(x_q, x_scale, w_q, w_scale, bias, addend, out_dtype, out)
-    out = _out(out, "out", shape, out_dtype, x_q)
+    shape = (*x_scale.shape, N)
+    out = x_q.new_empty(shape, dtype=out_dtype) if out is None else _out(out, "out", shape, out_dtype, x_q)
     dims = mate_linear_i8_dims(x_scale.numel(), K, N, _DT[out_dtype])
-    mate_linear_i8_fwd(x_q, x_scale, w_q, w_scale, bias, addend, out, dims, _current(x_q))
+    rc = _lib.load().mate_linear_i8_fwd(x_q.data_ptr(), x_scale.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(),
+                                        _addr(bias), _addr(addend), out.data_ptr(), ctypes.byref(dims), _current(dev))
+    check("mate_linear_i8_fwd", rc)
     return out
 
 
@@ -369,16 +389,43 @@ def gate_norm_i8(y, z, w, group: int, eps: float = 1e-5, stream=None) -> Codes:
     if z.shape != y.shape or w.shape != (y.shape[-1],):
         raise ValueError("y and z must have one shape and w one entry per channel")
     _same_device(y, z, w)
-    if _elsewhere(y, stream):
+    dev = y.get_device()
+    if stream is not None or dev != torch._C._cuda_getDevice():
         with _on(y, stream):
             return gate_norm_i8(y, z, w, group, eps)
-    *lead, C = y.shape
-    q, scale = y.new_empty(y.shape, dtype=torch.int8), y.new_empty(lead, dtype=torch.float32)
-    mate_gate_norm_i8_fwd(y, z, w, eps, q, scale, mate_gate_norm_dims(_rows(lead), C, int(group), MATE_BF16), _current(y))
+    q, scale = torch.empty_like(y, dtype=torch.int8), y.new_empty(y.shape[:-1], dtype=torch.float32)
+    dims = mate_gate_norm_dims(scale.numel(), y.shape[-1], int(group), MATE_BF16)
+    rc = _lib.load().mate_gate_norm_i8_fwd(y.data_ptr(), z.data_ptr(), w.data_ptr(), float(eps), q.data_ptr(),
+                                           scale.data_ptr(), ctypes.byref(dims), _current(dev))
+    check("mate_gate_norm_i8_fwd", rc)
     return Codes(q, scale)
 
 
 _NORMS = {"rms": MATE_NORM_RMS, "layer": MATE_NORM_LAYER}
+
+
+def _check_vec(t, name, C, dev):
+    """A weight of block_norm: its address."""
+    if t is None:
+        return None
+    _require(t, name, torch.float32)
+    if t.shape != (C,):
+        raise ValueError(f"{name} must have one entry per channel")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    return t.data_ptr()
+
+
+def _check_mod(t, name, batch, C, dev):
+    """A modulation vector of block_norm: its address and its stride between batch elements."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.float32 or t.get_device() != dev:
+        raise ValueError(f"{name} must be a float32 CUDA tensor on cuda:{dev}")
+    n = t.dim()
+    if t.shape != ((batch, C) if n == 2 else (C,)) or (C > 1 and t.stride(n - 1) != 1):
+        raise ValueError(f"{name} must be (batch, C) or (C,), its channels contiguous")
+    return t.data_ptr(), t.stride(0) if n == 2 and batch > 1 else 0
 
 
 def block_norm(x, y=None, *, w_post=None, gate=None, residual_scale: float = 1.0, post_norm: bool = True, w_pre=None,
@@ -395,56 +442,45 @@ def block_norm(x, y=None, *, w_post=None, gate=None, residual_scale: float = 1.0
     (no h). x_out may be x. Returns (x_out or None, h or None)."""
     if norm not in _NORMS:
         raise ValueError(f"norm must be one of {sorted(_NORMS)}, got {norm!r}")
-    if h_dtype not in (torch.bfloat16, torch.int8, None):
+    if h_dtype is None:
+        if w_pre is not None or scale is not None or shift is not None:
+            raise ValueError("w_pre, scale and shift go with h")
+        if y is None:
+            raise ValueError("nothing to compute: neither y nor h")
+    elif h_dtype is not torch.bfloat16 and h_dtype is not torch.int8:
         raise ValueError(f"h_dtype must be bfloat16, int8 or None, got {h_dtype}")
     if y is None and (w_post is not None or gate is not None or x_out is not None or residual_scale != 1.0):
         raise ValueError("w_post, gate, residual_scale and x_out go with y")
-    if h_dtype is None and (w_pre is not None or scale is not None or shift is not None):
-        raise ValueError("w_pre, scale and shift go with h")
-    if y is None and h_dtype is None:
-        raise ValueError("nothing to compute: neither y nor h")
     _require(x, "x")
     if x.dtype not in _DT or x.dim() < 2:
         raise ValueError(f"x must be (batch, ..., C) bfloat16 or float32, got {x.dtype}")
-    batch, *inner, C = x.shape
+    dev, shape = x.get_device(), x.shape
+    batch, C = shape[0], shape[-1]
     if y is not None:
         _require(y, "y", torch.bfloat16)
-        if y.shape != x.shape:
-            raise ValueError("x and y must have one shape")
+        if y.shape != shape or y.get_device() != dev:
+            raise ValueError("x and y must have one shape and be on one device")
         if w_post is not None and not post_norm:
             raise ValueError("w_post goes with post_norm")
-    for t, n in ((w_post, "w_post"), (w_pre, "w_pre")):
-        if t is not None:
-            _require(t, n, torch.float32)
-            if t.shape != (C,):
-                raise ValueError(f"{n} must have one entry per channel")
-    strides = []
-    for t, n in ((gate, "gate"), (scale, "scale"), (shift, "shift")):
-        if t is None:
-            strides.append(0)
-            continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32:
-            raise ValueError(f"{n} must be a float32 CUDA tensor")
-        if t.shape not in ((batch, C), (C,)) or (C > 1 and t.stride(-1) != 1):
-            raise ValueError(f"{n} must be (batch, C) or (C,), its channels contiguous")
-        strides.append(0 if t.dim() == 1 or batch == 1 else t.stride(0))
-    _same_device(x, y, w_post, gate, w_pre, scale, shift)
-    if _elsewhere(x, stream):
+    p_post, p_pre = _check_vec(w_post, "w_post", C, dev), _check_vec(w_pre, "w_pre", C, dev)
+    p_gate, s_gate = _check_mod(gate, "gate", batch, C, dev)
+    p_scale, s_scale = _check_mod(scale, "scale", batch, C, dev)
+    p_shift, s_shift = _check_mod(shift, "shift", batch, C, dev)
+    if stream is not None or dev != torch._C._cuda_getDevice():
         with _on(x, stream):
             return block_norm(x, y, w_post=w_post, gate=gate, residual_scale=residual_scale, post_norm=post_norm,
                               w_pre=w_pre, scale=scale, shift=shift, norm=norm, eps=eps, h_dtype=h_dtype, x_out=x_out)
-    h = h_scale = None
     if y is not None:
-        x_out = _out(x_out, "x_out", x.shape, x.dtype, x)
-    if h_dtype is not None:
-        h = x.new_empty(x.shape, dtype=h_dtype)
-        if h_dtype == torch.int8:
-            h_scale = x.new_empty(x.shape[:-1], dtype=torch.float32)
-    kind = _NORMS[norm]
-    dims = mate_block_norm_dims(batch, _rows(inner), C, kind if post_norm else MATE_NORM_NONE, kind, _DT[x.dtype],
-                                MATE_I8 if h_scale is not None else MATE_BF16, *strides, residual_scale, eps)
-    mate_block_norm_fwd(x, y, w_post, gate, w_pre, scale, shift, x_out, h, h_scale, dims, _current(x))
-    return x_out, (Codes(h, h_scale) if h_scale is not None else h)
+        x_out = torch.empty_like(x) if x_out is None else _out(x_out, "x_out", shape, x.dtype, x)
+    h = None if h_dtype is None else torch.empty_like(x, dtype=h_dtype)
+    h_scale = x.new_empty(shape[:-1], dtype=torch.float32) if h_dtype is torch.int8 else None
+    kind, rows = _NORMS[norm], _rows(shape[1:-1])
+    dims = mate_block_norm_dims(batch, rows, C, kind if post_norm else MATE_NORM_NONE, kind, _DT[x.dtype],
+                                MATE_BF16 if h_scale is None else MATE_I8, s_gate, s_scale, s_shift, residual_scale, eps)
+    rc = _lib.load().mate_block_norm_fwd(x.data_ptr(), _addr(y), p_post, p_gate, p_pre, p_scale, p_shift, _addr(x_out),
+                                         _addr(h), _addr(h_scale), ctypes.byref(dims), _current(dev))
+    check("mate_block_norm_fwd", rc)
+    return x_out, (h if h_scale is None else Codes(h, h_scale))
 
 
 # the block's weights that its matrix products read

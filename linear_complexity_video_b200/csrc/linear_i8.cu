@@ -294,23 +294,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const float xs = m0 + row < geo.M ? geo.x_scale[m0 + row] : 0.f;
             if (!tc::named_all(1 + g, 128, tc::mbar_wait_sleep(&bars[kBarAccFull + acc], use & 1u, err, abort_flag))) break;
             tc::tc_fence_after();
-            // the accumulator goes back to the MMAs (of the tile after next) once this group has its
-            // last chunk of it in registers
-            auto release = [&] {
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive_cluster(tc::cluster_addr(&bars[kBarAccEmpty + acc], 0));
-            };
-            if (g >= chunks) release();
-            for (int c = g; c < chunks; c += kGroups, ++done) {
+            // the group's columns, all at once, and the accumulator goes back to the MMAs (of the
+            // tile after next)
+            constexpr int kOwn = 128 / kOutCols;  // chunks of a full tile that are the group's
+            uint32_t v[kOwn][kOutCols / 32][32];
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) {
+                const int c = kGroups * i + g;
+                if (c < chunks) {
+#pragma unroll
+                    for (int q = 0; q < kOutCols / 32; ++q)
+                        tc::tmem_ld32u(tc::tmem_addr(tmem + acc * kBN, lane_base, kOutCols * c + 32 * q), v[i][q]);
+                }
+            }
+            tc::tmem_wait_ld();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_cluster(tc::cluster_addr(&bars[kBarAccEmpty + acc], 0));
+#pragma unroll
+            for (int i = 0; i < kOwn; ++i) {
+                const int c = kGroups * i + g;
+                if (c >= chunks) break;
                 const uint32_t slot = done % kSlots;
                 const int n0 = at.n + kOutCols * c;
-                uint32_t v[kOutCols / 32][32];
-#pragma unroll
-                for (int q = 0; q < kOutCols / 32; ++q)
-                    tc::tmem_ld32u(tc::tmem_addr(tmem + acc * kBN, lane_base, kOutCols * c + 32 * q), v[q]);
-                tc::tmem_wait_ld();
-                if (c + kGroups >= chunks) release();
                 if (geo.has_addend) {
                     if (et == 0) {
                         tc::bulk_wait_read<0>();  // the other slot is free again: the next chunk's addend
@@ -323,12 +329,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     tc::named_sync(1 + g, 128);
                 }
                 uint8_t *stg = slots + slot * kOutTile;
-                const float *cv = vec + c / kGroups * kOutCols;
+                const float *cv = vec + i * kOutCols;
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     uint4 *to = reinterpret_cast<uint4 *>(stg + tc::sw128(row, q));
                     // columns past N hold zeros and are not written
-                    *to = finish<F32>(&v[q * (kOutCols / 8) / 32][q * (kOutCols / 8) % 32], xs, cv + q * (kOutCols / 8), geo, to);
+                    *to = finish<F32>(&v[i][q * (kOutCols / 8) / 32][q * (kOutCols / 8) % 32], xs, cv + q * (kOutCols / 8), geo, to);
                 }
                 tc::fence_proxy_async_smem();
                 tc::named_sync(1 + g, 128);
@@ -337,12 +343,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                     if (m0 < geo.M) tc::tma_store_2d(&mo, stg, n0, m0);
                     tc::bulk_commit();
                 }
+                ++done;
             }
         }
         if (et == 0) {
-            // the addends asked for have landed (bounded), the stores have completed
+            // the addends asked for have landed (bounded), the stores have left shared memory
             for (uint32_t i = done; i < asked; ++i) tc::mbar_wait(&add[i % kSlots], (i / kSlots) & 1u, nullptr);
-            tc::bulk_wait_all();
+            tc::bulk_wait_read_all();
         }
     }
 
