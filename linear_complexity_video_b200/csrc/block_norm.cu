@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(TPR *ROWS, CTAS) block_norm_kernel(BlockNormAr
             unpack8(xv[j], f);
         }
     };
+    tc::stream_release();  // a product behind it may set itself up
     if (r0 + slot < r1) load(r0 + slot);
     {
         const float *gate = a.gate + (int64_t)b * a.gate_stride, *scale = a.scale + (int64_t)b * a.scale_stride,

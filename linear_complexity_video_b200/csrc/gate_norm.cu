@@ -131,6 +131,7 @@ __global__ void __launch_bounds__(kGnThreads, VPL <= 2 ? 6 : VPL <= 5 ? 4 : 2) g
             zv[j] = v < nv ? __ldcs(z + v) : make_uint4(0, 0, 0, 0);
         }
     };
+    tc::stream_release();  // a product behind it may set itself up
     load(blockIdx.x);
     for (int64_t r = blockIdx.x; r < a.M; r += gridDim.x) {
         float2 g[VPL][4];

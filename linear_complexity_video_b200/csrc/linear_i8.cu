@@ -41,6 +41,7 @@
 // own waits by the same limit) and frees its TMEM.
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.h"
 #include "tc.cuh"
 #include "tmap.h"
 
@@ -153,6 +154,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     constexpr int kOutCols = F32 ? 32 : 64;  // columns of a staging tile
     extern __shared__ __align__(1024) uint8_t base[];
     if (tc::smem_u32(base) & 1023u) {  // the swizzled tiles need it; the same for every thread of both CTAs
+        tc::stream_wait();
         if (threadIdx.x == 0) atomicExch(err, MATE_ERR_INVALID_ARG);
         return;
     }
@@ -189,6 +191,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tc::cluster_sync();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    tc::stream_wait();
+    tc::stream_release();
 
     if (warp == 0) {
         // ---------------- TMA producer ----------------
@@ -401,8 +405,7 @@ cudaError_t launch_linear_i8(const LinearI8Args &a, cudaStream_t s)
     geo.has_addend = a.addend != nullptr;
     const int grid = 2 * std::min(geo.tiles, std::max(nsm / 2, 1));
     Phase ph(a.phase ? a.phase : MATE_PHASE_LINEAR_I8, s);
-    kernel<<<grid, kThreads, kSmemBytes, s>>>(ma, mb, mo, md, geo, a.err);
-    return cudaGetLastError();
+    return launch_in_stream(kernel, dim3(grid), kThreads, kSmemBytes, 0, s, ma, mb, mo, md, geo, a.err);
 }
 
 }  // namespace mate

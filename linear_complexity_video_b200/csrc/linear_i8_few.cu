@@ -18,6 +18,7 @@
 // that every CTA of a cluster reaches the cluster's barriers.
 #include "common.cuh"
 #include "kernels.h"
+#include "launch.h"
 #include "tc.cuh"
 #include "tmap.h"
 
@@ -82,6 +83,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    tc::stream_wait();
+    tc::stream_release();
 
     if (tid == 0) {
         int it = 0;
@@ -216,19 +219,9 @@ template <int NT> cudaError_t launch(const LinearI8Args &a, int nsm, cudaStream_
     // 6.1 us; 64 tokens 10.4, 8.5, 7.3, 9.0; 7,680 -> 2,560, 64 tokens 21, 14, 10, 11)
     int splits = 1;
     while (splits < 4 && 2 * splits <= geo.nk && 2 * splits * tiles <= 2 * nsm) splits *= 2;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * splits));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Few<NT>::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = splits;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = splits > 1 ? 1 : 0;
     Phase ph(a.phase ? a.phase : MATE_PHASE_LINEAR_I8, s);
-    return cudaLaunchKernelEx(&cfg, kernel, mx, mw, geo, splits, a.err);
+    return launch_in_stream(kernel, dim3((unsigned)(tiles * splits)), kThreads, Few<NT>::kSmem, splits, s, mx, mw, geo, splits,
+                            a.err);
 }
 
 }  // namespace

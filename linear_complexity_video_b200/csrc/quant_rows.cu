@@ -38,6 +38,7 @@ __global__ void __launch_bounds__(kQThreads) quant_rows_kernel(QuantArgs a)
     const bool live = row < a.M;
     const int nv = live ? a.K / 8 : 0;
     const uint4 *x = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.x) + row * a.K);
+    tc::stream_release();  // a product behind it may set itself up
     uint4 v[VPL];
 #pragma unroll
     for (int j = 0; j < VPL; ++j) v[j] = t + j * TPR < nv ? __ldcs(x + t + j * TPR) : make_uint4(0, 0, 0, 0);

@@ -43,6 +43,16 @@ __device__ __forceinline__ uint64_t globaltimer()
 __host__ __device__ __forceinline__ uint32_t sw128(uint32_t r, uint32_t c) { return r * 128u + ((c ^ (r & 7u)) << 4); }
 
 // ---------------------------------------------------------------------------
+// stream order, for kernels launched with programmatic stream serialisation (launch.h)
+// ---------------------------------------------------------------------------
+// Every thread calls this before it touches global memory or starts a bounded wait: the
+// grids ahead in the stream have completed and their writes are visible.
+__device__ __forceinline__ void stream_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// A next grid that is launched so may have its CTAs placed (their stream_wait still waits for
+// all of this one).
+__device__ __forceinline__ void stream_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// ---------------------------------------------------------------------------
 // mbarriers
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void mbar_init(uint64_t *bar, uint32_t count)

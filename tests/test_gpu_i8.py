@@ -161,12 +161,39 @@ def test_linear_i8_is_reproducible_and_keeps_nan_rows():
     assert torch.isnan(a[3]).all() and (a[4] == 0).all() and torch.isfinite(a[5:]).all()
 
 
-def test_linear_i8_leading_shape():
+def test_leading_shapes():
     xq, xs, wq, ws, _, _ = _linear_inputs(24, 64, 40, seed=6)
     d = [t.cuda() for t in (xq, xs, wq, ws)]
     a = mate.linear_i8(*d)
     b = mate.linear_i8(d[0].view(2, 3, 4, 64), d[1].view(2, 3, 4), d[2], d[3])
     assert b.shape == (2, 3, 4, 40) and torch.equal(a, b.view(24, 40))
+    # a single row without a leading dimension
+    one = mate.linear_i8(d[0][5], d[1][5], d[2], d[3])
+    assert one.shape == (40,) and torch.equal(one, a[5])
+    x = torch.randn(3, 5, 64, generator=_gen(1)).to(torch.bfloat16).cuda()
+    c, r = mate.quantize_rows(x), mate.quantize_rows(x[1, 2])
+    assert c.scale.shape == (3, 5) and r.scale.shape == ()
+    assert torch.equal(c.q[1, 2], r.q) and torch.equal(c.scale[1, 2], r.scale)
+
+
+def test_refusals_on_the_device():
+    xq, xs, wq, ws, bias, addend = [t.cuda() for t in _linear_inputs(8, 64, 40, seed=7)]
+    ok = dict(x_q=xq, x_scale=xs, w_q=wq, w_scale=ws)
+    for kw in (dict(x_q=xq.float()), dict(x_q=xq[:, :32]), dict(x_q=xq.t()), dict(x_scale=xs[:4]), dict(x_scale=xs.double()),
+               dict(x_scale=xs[:, None]), dict(w_q=wq[0]), dict(w_scale=ws[:8]), dict(bias=bias[:8]), dict(bias=bias.half()),
+               dict(addend=addend[:4]), dict(addend=addend.float()), dict(out_dtype=torch.float16), dict(x_q=None),
+               dict(out=torch.empty(8, 48, dtype=torch.bfloat16, device="cuda")), dict(x_scale=xs.cpu())):
+        with pytest.raises(ValueError):
+            mate.linear_i8(**{**ok, **kw})
+    # no rows; rows of codes off the 16-byte boundary; an output over an input
+    for kw in (dict(x_q=xq[:0], x_scale=xs[:0]), dict(x_q=torch.empty(8 * 64 + 8, dtype=torch.int8, device="cuda")[8:].view(8, 64)),
+               dict(out=xq.view(torch.bfloat16).flatten()[:1].expand(1), x_q=xq[:1], x_scale=xs[:1], w_q=wq[:1], w_scale=ws[:1])):
+        with pytest.raises((mate.MateError, ValueError)):
+            mate.linear_i8(**{**ok, **kw})
+    with pytest.raises(mate.MateError):
+        mate.quantize_rows(torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(mate.MateError):
+        mate.quantize_rows(torch.zeros(4, 60, dtype=torch.bfloat16, device="cuda"))
 
 
 @pytest.mark.slow
@@ -281,6 +308,34 @@ def test_two_streams_at_once(M):
     for k in range(2):
         for outs in got[k]:
             assert all(torch.equal(a, b) for a, b in zip(outs, want[k]))
+
+
+@pytest.mark.parametrize("M", [5, 300, 6000])
+def test_reused_buffers_keep_stream_order(M):
+    """Products and quantisations that read and overwrite the same few buffers, forty calls without a
+    wait between them: what waiting after every call gives, bit for bit (the products are launched
+    so that they may set themselves up before the call ahead of them has ended)."""
+    g = _gen(M)
+    w = [mate.quantize_rows((torch.randn(256, 256, generator=g) / 16).to(torch.bfloat16).cuda()) for _ in range(2)]
+    x0 = torch.randn(M, 256, generator=g).to(torch.bfloat16).cuda()
+
+    def run(wait):
+        a, b = x0.clone(), torch.empty_like(x0)
+        q, s = torch.empty(M, 256, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda")
+        dims = mate.api.mate_quant_dims(M, 256, 1)
+        for i in range(20):
+            mate.mate_quant_rows_fwd(a, q, s, dims)
+            wait()
+            mate.linear_i8(q, s, *w[i % 2], out=b)
+            wait()
+            mate.linear_i8(q, s, *w[(i + 1) % 2], addend=b, out=b)
+            wait()
+            a, b = b, a
+        return a
+
+    slow = run(torch.cuda.synchronize)
+    fast = run(lambda: None)
+    assert torch.equal(slow, fast) and torch.isfinite(fast).all()
 
 
 def test_two_graphs_of_one_workspace_free_chain():
