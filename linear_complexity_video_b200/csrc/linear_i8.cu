@@ -31,9 +31,11 @@
 // change); tiles of 256 x 512 with x loaded once for both halves (a quarter less to load: 476 us
 // against 492 for 32,768 tokens, 7,680 -> 2,560, but 181 against 175 at K = 2,560, since one tile
 // fills TMEM and its epilogue is exposed).
-// Tiles are walked in groups of eight tile rows, so that the 74 pairs at work read about
-// eight rows' x and nine columns' w from L2 (in_proj of 131,072 tokens: 3.30 ms row by row,
-// 3.20 in groups).
+// Tiles are walked in groups of four tile rows, so that the 74 pairs at work read about
+// four rows' x and 19 columns' w from L2 (65,536 tokens, 2,560 -> 10,448, in a graph: 1,370 us
+// in groups of 4, 1,399 of 8, 1,390 of 16, 1,378 of 32; 32,768 tokens, 7,680 -> 2,560: 484, 483,
+// 493, 540. Row by row, on an earlier form, in_proj of 131,072 tokens took 3.30 ms where groups of
+// 8 took 3.20).
 //
 // Every wait is bounded (2 s); a wait that gives up records MATE_ERR_TIMEOUT and
 // raises a CTA abort flag that makes every role leave its loop; the CTA then
@@ -54,7 +56,7 @@ namespace {
 constexpr int kBM = 256, kBK = 128;                  // rows of a pair's tile; a K step is 128 codes = one swizzled row
 constexpr int kBN = 256;                             // columns of a tile
 constexpr int kStages = 5, kGroups = 2, kSlots = 2;  // staging tiles per epilogue group
-constexpr int kGroup = 8;                            // tile rows walked together
+constexpr int kGroup = 4;                            // tile rows walked together
 constexpr uint32_t kTile = 128 * kBK;                // 16 KB: one CTA's part of x or w
 constexpr uint32_t kStage = 2 * kTile;
 constexpr uint32_t kOutTile = 128 * 128;             // 16 KB: 128 rows x 128 bytes

@@ -372,3 +372,28 @@ def test_stream_argument(as_handle):
     got = mate.linear_i8(*mate.quantize_rows(x, stream=arg), *w, stream=arg)
     st.synchronize()
     assert torch.equal(got, want)
+
+
+def test_several_host_threads():
+    import threading
+
+    xq, xs, wq, ws, _, _ = [t.cuda() for t in _linear_inputs(9000, 256, 136, seed=8)]
+    x = torch.randn(40, 256, generator=_gen(9)).to(torch.bfloat16).cuda()
+    want = (mate.linear_i8(xq, xs, wq, ws), mate.linear_i8(xq[:40], xs[:40], wq, ws), *mate.quantize_rows(x))
+    torch.cuda.synchronize()
+    got = []
+
+    def work():
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            for _ in range(20):
+                r = (mate.linear_i8(xq, xs, wq, ws), mate.linear_i8(xq[:40], xs[:40], wq, ws), *mate.quantize_rows(x))
+        st.synchronize()
+        got.append(r)
+
+    threads = [threading.Thread(target=work) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert len(got) == 4 and all(torch.equal(a, b) for r in got for a, b in zip(r, want))
