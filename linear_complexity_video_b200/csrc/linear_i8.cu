@@ -40,7 +40,8 @@
 // Every wait is bounded (2 s); a wait that gives up records MATE_ERR_TIMEOUT and
 // raises a CTA abort flag that makes every role leave its loop; the CTA then
 // waits (bounded) for its copies and MMAs in flight, meets its peer (which leaves its
-// own waits by the same limit) and frees its TMEM.
+// own waits by the same limit), waits (bounded) for the arrivals that the MMA thread's
+// commits still owe its own barriers, and frees its TMEM.
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.h"
@@ -64,9 +65,10 @@ constexpr uint32_t kOffStages = 0;
 constexpr uint32_t kOffOut = kStages * kStage;
 constexpr uint32_t kOffVec = kOffOut + kGroups * kSlots * kOutTile;  // per group: w_scale and bias of its columns
 constexpr uint32_t kOffBar = kOffVec + 2 * kBN * 4;
-// full, empty (per stage), acc_full[2], acc_empty[2], addend (per slot), drain; then the TMEM slot and the abort flag
+// full, empty (per stage), acc_full[2], acc_empty[2], addend (per slot), drain
 constexpr int kBarFull = 0, kBarEmpty = kStages, kBarAccFull = 2 * kStages, kBarAccEmpty = 2 * kStages + 2,
               kBarAdd = 2 * kStages + 4, kBarDrain = kBarAdd + kGroups * kSlots, kNumBars = kBarDrain + 1;
+// the TMEM slot, the abort flag, and what rank 0's MMA thread committed: stages, accumulators
 constexpr uint32_t kOffMisc = kOffBar + 8 * kNumBars;
 constexpr uint32_t kSmemBytes = kOffMisc + 16;
 static_assert(kSmemBytes <= 227 * 1024, "linear_i8: shared memory");
@@ -163,6 +165,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(base + kOffBar);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(base + kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(base + kOffMisc + 4);
+    uint32_t *commits = reinterpret_cast<uint32_t *>(base + kOffMisc + 8);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = (int)tc::cluster_rank(), pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -226,7 +229,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ---------------- MMA issue ----------------
         if (lane == 0 && rank == 0) {
             const uint32_t idesc = tc::idesc_i8(kBM, kBN);
-            uint32_t it = 0, tl = 0, committed = 0;
+            uint32_t it = 0, tl = 0, committed = 0, filled = 0;
             for (int t = pair; t < geo.tiles && !*abort_flag; t += pairs, ++tl) {
                 const uint32_t acc = tl & 1, use = tl >> 1;
                 if (use > 0 && !tc::mbar_wait_or_abort(&bars[kBarAccEmpty + acc], (use - 1) & 1u, err, abort_flag))
@@ -251,11 +254,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 if (!ok) break;
                 tc::mma_commit_pair(&bars[kBarAccFull + acc]);
+                ++filled;
             }
             // every MMA issued has completed before TMEM may be freed (bounded)
             if (committed > 0) {
                 tc::mma_commit_pair(&bars[kBarDrain]);
                 tc::mbar_wait(&bars[kBarDrain], 0, nullptr);
+            }
+            for (uint32_t r = 0; r < 2; ++r) {
+                tc::st_cluster(tc::cluster_addr(&commits[0], r), committed);
+                tc::st_cluster(tc::cluster_addr(&commits[1], r), filled);
             }
         }
     } else {
@@ -361,8 +369,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     tc::tc_fence_before();
     __syncthreads();
-    tc::cluster_sync();  // the peer's loads, commits and arrivals reach this CTA's shared memory until here
-    if (warp == 1) {
+    // the peer's loads have landed and its threads' stores and arrivals are done; the arrivals of
+    // commits are not part of it: they come by themselves, at each CTA in its own time
+    tc::cluster_sync();
+    if (warp == 0) {
+        // Every commit has arrived on this CTA's barriers before its shared memory may go to
+        // another CTA. Commit j of a stage or an accumulator is issued only after commit j - 1
+        // was seen in both CTAs, so at most the last phase of each barrier is outstanding.
+        const uint32_t first = lane < kStages ? lane : lane - kStages, of = lane < kStages ? kStages : 2;
+        const uint32_t issued = lane < kStages ? commits[0] : lane < kStages + 2 ? commits[1] : 0;
+        if (issued > first)
+            tc::mbar_wait(&bars[lane < kStages ? kBarEmpty + lane : kBarAccFull + first], ((issued - 1 - first) / of) & 1u, err);
+        if (lane == kStages + 2 && commits[0] > 0) tc::mbar_wait(&bars[kBarDrain], 0, err);
+    } else if (warp == 1) {
         tc::tc_fence_after();
         tc::tmem_dealloc_pair(tmem, kTmemCols);
     }

@@ -561,6 +561,12 @@ __device__ __forceinline__ int4 ld_cluster(uint32_t addr)
     return v;
 }
 
+// 4 bytes into a CTA's shared memory (a cluster_addr)
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_addr)
 {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_addr) : "memory");
@@ -602,6 +608,7 @@ __device__ __forceinline__ void mma_i8_pair(uint32_t d_tmem, uint64_t adesc, uin
 }
 
 // Arrive on `bar` of both CTAs once all previously issued pair MMAs of this thread complete.
+// Asynchronous in each of them: that one has seen its arrival says nothing of the other.
 __device__ __forceinline__ void mma_commit_pair(uint64_t *bar)
 {
     asm volatile(

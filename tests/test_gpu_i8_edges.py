@@ -1,0 +1,71 @@
+"""The 8-bit operators at their edges: calls that follow one another without a wait, codes and sizes
+at the limits, gates far from zero."""
+import numpy as np
+import pytest
+import torch
+
+import plain64
+from gpu_util import host64
+
+pytestmark = pytest.mark.gpu
+
+mate = pytest.importorskip("linear_complexity_video_b200")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    mate.load()
+
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _product(M, K, N, seed):
+    g = _gen(seed)
+    codes = lambda *s: torch.randint(-127, 128, s, generator=g, dtype=torch.int8, device="cuda")  # noqa: E731
+    return (codes(M, K), torch.rand(M, generator=g, device="cuda") + 0.01, codes(N, K),
+            torch.rand(N, generator=g, device="cuda") + 0.01)
+
+
+# Products of the CTA pairs' kernel, where the commits of one CTA arrive at both: one K step (the last
+# commits are on their way when the tile's epilogue starts), as many as the ring has stages, one more, and
+# many; a single tile column whose second half is empty, and several; pairs with one tile and with several.
+PAIRS = [(19200, 128, 128), (19200, 640, 64), (9001, 768, 520), (40000, 16, 264), (6401, 1296, 1000)]
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_products_on_the_heels_of_one_another(captured):
+    """A CTA leaves its SM only when nothing more arrives in its shared memory: the next product's CTAs
+    have their barriers at the same places. Sixty products without a wait, eager or in one graph,
+    against each after a wait."""
+    ins = [_product(*s, seed=i) for i, s in enumerate(PAIRS)]
+    want = []
+    for a in ins:
+        want.append(mate.linear_i8(*a, out_dtype=torch.float32))
+        torch.cuda.synchronize()
+    for (xq, xs, wq, ws), w in zip(ins, want):
+        rows = [0, 127, 128, 255, 256, w.shape[0] - 1]
+        ref, tol = plain64.linear(*(t.cpu() for t in (xq[rows], xs[rows], wq, ws)))
+        assert (np.abs(host64(w[rows]) - ref) <= tol + plain64.U * (np.abs(ref) + tol)).all()
+    outs = [torch.empty_like(w) for w in want for _ in range(12)]
+
+    def run():
+        for i, out in enumerate(outs):
+            k = i % len(ins)
+            mate.linear_i8(*ins[k], out_dtype=torch.float32, out=outs[12 * k + i // len(ins)])
+
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+        run = graph.replay
+    for _ in range(5):
+        for out in outs:
+            out.fill_(-1.0)
+        run()
+        torch.cuda.synchronize()
+        assert mate.mate_last_error() == 0
+        assert all(torch.equal(out, want[i // 12]) for i, out in enumerate(outs))
