@@ -98,6 +98,10 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
         // every load issued has landed before the ring gives way (bounded)
         tc::mbar_wait(&full[(it - 1) % L::kStages], ((it - 1) / L::kStages) & 1, nullptr);
+        // and the last commit of each stage has arrived before the CTA may leave (the loads above
+        // waited for the earlier ones)
+        for (int s = 0; s < L::kStages && s < it; ++s)
+            if (!tc::mbar_wait_or_abort(&empty[s], ((it - 1 - s) / L::kStages) & 1, err, abort_flag)) break;
     } else if (tid == 32) {
         const uint32_t idesc = tc::idesc_i8(kBC, NT);
         for (int k = k0, it = 0; k < k1; ++k, ++it) {

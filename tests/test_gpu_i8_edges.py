@@ -34,20 +34,24 @@ def _product(M, K, N, seed):
 # commits are on their way when the tile's epilogue starts), as many as the ring has stages, one more, and
 # many; a single tile column whose second half is empty, and several; pairs with one tile and with several.
 PAIRS = [(19200, 128, 128), (19200, 640, 64), (9001, 768, 520), (40000, 16, 264), (6401, 1296, 1000)]
+# Those of the few-token kernel: one K step, fewer than its ring's stages, as many, many; one, two and
+# four CTAs to a tile; tiles of 16, 32 and 64 tokens.
+FEW = [(3, 128, 136), (16, 256, 2560), (30, 768, 18944), (64, 2560, 2560), (300, 1296, 1000)]
 
 
 @pytest.mark.parametrize("captured", [False, True])
-def test_products_on_the_heels_of_one_another(captured):
+@pytest.mark.parametrize("shapes", [PAIRS, FEW], ids=["pairs", "few"])
+def test_products_on_the_heels_of_one_another(shapes, captured):
     """A CTA leaves its SM only when nothing more arrives in its shared memory: the next product's CTAs
     have their barriers at the same places. Sixty products without a wait, eager or in one graph,
     against each after a wait."""
-    ins = [_product(*s, seed=i) for i, s in enumerate(PAIRS)]
+    ins = [_product(*s, seed=i) for i, s in enumerate(shapes)]
     want = []
     for a in ins:
         want.append(mate.linear_i8(*a, out_dtype=torch.float32))
         torch.cuda.synchronize()
     for (xq, xs, wq, ws), w in zip(ins, want):
-        rows = [0, 127, 128, 255, 256, w.shape[0] - 1]
+        rows = sorted({min(r, w.shape[0] - 1) for r in (0, 127, 128, 255, 256, w.shape[0])})
         ref, tol = plain64.linear(*(t.cpu() for t in (xq[rows], xs[rows], wq, ws)))
         assert (np.abs(host64(w[rows]) - ref) <= tol + plain64.U * (np.abs(ref) + tol)).all()
     outs = [torch.empty_like(w) for w in want for _ in range(12)]
