@@ -41,7 +41,7 @@ def _ptr(t: Optional[torch.Tensor]) -> ctypes.c_void_p:
 def _int3(v: Optional[Sequence[int]]):
     if v is None:
         return None
-    return (ctypes.c_int * 3)(*[int(u) for u in v])
+    return (ctypes.c_int * 3)(*[_lib.Int.from_param(int(u)) for u in v])
 
 
 def _require(t: torch.Tensor, name: str, dtype=None):
@@ -313,8 +313,8 @@ def quantize_rows(x, stream=None) -> Codes:
     if stream is not None or dev != torch._C._cuda_getDevice():
         with _on(x, stream):
             return quantize_rows(x)
+    dims = mate_quant_dims.of(_rows(x.shape[:-1]), x.shape[-1], MATE_BF16)
     q, scale = torch.empty_like(x, dtype=torch.int8), x.new_empty(x.shape[:-1], dtype=torch.float32)
-    dims = mate_quant_dims(scale.numel(), x.shape[-1], MATE_BF16)
     rc = _lib.load().mate_quant_rows_fwd(x.data_ptr(), q.data_ptr(), scale.data_ptr(), ctypes.byref(dims), _current(dev))
     check("mate_quant_rows_fwd", rc)
     return Codes(q, scale)
@@ -371,9 +371,9 @@ def linear_i8(x_q, x_scale, w_q, w_scale, bias=None, addend=None, out_dtype=torc
     if stream is not None or dev != torch._C._cuda_getDevice():
         with _on(x_q, stream):
             return linear_i8(x_q, x_scale, w_q, w_scale, bias, addend, out_dtype, out)
+    dims = mate_linear_i8_dims.of(x_scale.numel(), K, N, _DT[out_dtype])
     shape = (*x_scale.shape, N)
     out = x_q.new_empty(shape, dtype=out_dtype) if out is None else _out(out, "out", shape, out_dtype, x_q)
-    dims = mate_linear_i8_dims(x_scale.numel(), K, N, _DT[out_dtype])
     rc = _lib.load().mate_linear_i8_fwd(x_q.data_ptr(), x_scale.data_ptr(), w_q.data_ptr(), w_scale.data_ptr(),
                                         _addr(bias), _addr(addend), out.data_ptr(), ctypes.byref(dims), _current(dev))
     check("mate_linear_i8_fwd", rc)
@@ -393,8 +393,8 @@ def gate_norm_i8(y, z, w, group: int, eps: float = 1e-5, stream=None) -> Codes:
     if stream is not None or dev != torch._C._cuda_getDevice():
         with _on(y, stream):
             return gate_norm_i8(y, z, w, group, eps)
+    dims = mate_gate_norm_dims.of(_rows(y.shape[:-1]), y.shape[-1], int(group), MATE_BF16)
     q, scale = torch.empty_like(y, dtype=torch.int8), y.new_empty(y.shape[:-1], dtype=torch.float32)
-    dims = mate_gate_norm_dims(scale.numel(), y.shape[-1], int(group), MATE_BF16)
     rc = _lib.load().mate_gate_norm_i8_fwd(y.data_ptr(), z.data_ptr(), w.data_ptr(), float(eps), q.data_ptr(),
                                            scale.data_ptr(), ctypes.byref(dims), _current(dev))
     check("mate_gate_norm_i8_fwd", rc)
@@ -470,13 +470,14 @@ def block_norm(x, y=None, *, w_post=None, gate=None, residual_scale: float = 1.0
         with _on(x, stream):
             return block_norm(x, y, w_post=w_post, gate=gate, residual_scale=residual_scale, post_norm=post_norm,
                               w_pre=w_pre, scale=scale, shift=shift, norm=norm, eps=eps, h_dtype=h_dtype, x_out=x_out)
+    kind, rows = _NORMS[norm], _rows(shape[1:-1])
+    dims = mate_block_norm_dims.of(batch, rows, C, kind if post_norm else MATE_NORM_NONE, kind, _DT[x.dtype],
+                                   MATE_I8 if h_dtype is torch.int8 else MATE_BF16, s_gate, s_scale, s_shift,
+                                   residual_scale, eps)
     if y is not None:
         x_out = torch.empty_like(x) if x_out is None else _out(x_out, "x_out", shape, x.dtype, x)
     h = None if h_dtype is None else torch.empty_like(x, dtype=h_dtype)
     h_scale = x.new_empty(shape[:-1], dtype=torch.float32) if h_dtype is torch.int8 else None
-    kind, rows = _NORMS[norm], _rows(shape[1:-1])
-    dims = mate_block_norm_dims(batch, rows, C, kind if post_norm else MATE_NORM_NONE, kind, _DT[x.dtype],
-                                MATE_BF16 if h_scale is None else MATE_I8, s_gate, s_scale, s_shift, residual_scale, eps)
     rc = _lib.load().mate_block_norm_fwd(x.data_ptr(), _addr(y), p_post, p_gate, p_pre, p_scale, p_shift, _addr(x_out),
                                          _addr(h), _addr(h_scale), ctypes.byref(dims), _current(dev))
     check("mate_block_norm_fwd", rc)

@@ -73,3 +73,24 @@ def test_products_on_the_heels_of_one_another(shapes, captured):
         torch.cuda.synchronize()
         assert mate.mate_last_error() == 0
         assert all(torch.equal(out, want[i // 12]) for i, out in enumerate(outs))
+
+
+def test_sizes_past_32_bits_are_refused():
+    """2^32 + 8 rows or channels, which would read as 8. The tensors are never read."""
+    e = lambda *s, dtype=torch.bfloat16: torch.empty(*s, dtype=dtype, device="cuda")  # noqa: E731
+    n = 2 ** 32 + 64
+    wide, codes, w = e(1, n), e(1, n, dtype=torch.int8), e(n, dtype=torch.float32)
+    one = e(1, dtype=torch.float32)
+    for call in (lambda: mate.quantize_rows(wide), lambda: mate.gate_norm_i8(wide, wide, w, n),
+                 lambda: mate.block_norm(wide, w_pre=w), lambda: mate.linear_i8(codes, one, e(8, n, dtype=torch.int8), w[:8]),
+                 lambda: mate.gate_norm(wide, wide, w, n), lambda: mate.linear(wide, wide)):
+        with pytest.raises(ValueError, match="does not fit"):
+            call()
+    del wide, codes, w
+    long = e(2 ** 32 + 8, 8)
+    for call in (lambda: mate.quantize_rows(long), lambda: mate.block_norm(long.view(1, -1, 8), h_dtype=torch.int8),
+                 lambda: mate.block_norm(long)):
+        with pytest.raises(ValueError, match="does not fit"):
+            call()
+    del long
+    torch.cuda.empty_cache()
