@@ -336,9 +336,10 @@ typedef struct {
  * 8-bit linear layer: a product of codes with a scale per token and a scale per
  * output channel,
  *     out_mn = x_scale_m w_scale_n sum_k x_mk w_nk (+ bias_n) (+ addend_mn)
- * with an exact sum (int32), scales, bias and addend in fp32, one rounding to
- * the output type. The addend serves an output that is the sum of products whose
- * inputs have scales of their own (the MATE composition of two branches).
+ * with an exact sum (of any int8 codes, -128 among them), scales, bias and addend in
+ * fp32, one rounding to the output type. The addend serves an output that is the sum
+ * of products whose inputs have scales of their own (the MATE composition of two
+ * branches).
  *   x       : (tokens, k) int8, row-major;  x_scale : (tokens) fp32
  *   w       : (n, k)      int8, row-major;  w_scale : (n)      fp32
  *   bias    : (n) fp32 or NULL

@@ -347,8 +347,8 @@ def _check_linear_i8(x_q, x_scale, w_q, w_scale, bias, addend, out_dtype):
 
 def linear_i8(x_q, x_scale, w_q, w_scale, bias=None, addend=None, out_dtype=torch.bfloat16,
               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """8-bit linear layer: x_scale w_scale (x_q w_q^T) + bias + addend, the sum exact and one
-    rounding to out_dtype (bf16 or fp32). x_q: (..., K) int8; x_scale: (...) fp32; w_q: (N, K)
+    """8-bit linear layer: x_scale w_scale (x_q w_q^T) + bias + addend, the sum exact (of any int8 codes)
+    and one rounding to out_dtype (bf16 or fp32). x_q: (..., K) int8; x_scale: (...) fp32; w_q: (N, K)
     int8; w_scale: (N,) fp32; bias: (N,) fp32; addend: (..., N) out_dtype, and may be `out`.
     Returns (..., N)."""
     try:

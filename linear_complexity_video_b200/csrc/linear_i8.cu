@@ -1,9 +1,10 @@
 // 8-bit linear layer on the 5th-generation tensor cores: a product of signed 8-bit
 // codes with a scale per token and a scale per output channel,
 //     out_mn = s_m t_n sum_k x_mk w_nk (+ bias_n) (+ addend_mn).
-// The sum is exact: kind::i8 accumulates in int32, and K <= 131,072 keeps
-// 127 * 127 * K below 2^31. The two scales, the bias and the addend are applied to it
-// in fp32 in the epilogue, and the result is rounded once to the output type.
+// The sum is exact: kind::i8 accumulates in int32, and for K <= 131,072 only the sum of
+// 131,072 products of -128 and -128 reaches 2^31 (tc::i8_sum). The two scales, the bias
+// and the addend are applied to it in fp32 in the epilogue, and the result is rounded once
+// to the output type.
 //
 // Persistent CTA pairs (clusters of two, cta_group::2), 320 threads per CTA; a pair
 // computes output tiles of 256 x 256, CTA r the rows 128 r ..:
@@ -74,7 +75,6 @@ constexpr uint32_t kSmemBytes = kOffMisc + 16;
 static_assert(kSmemBytes <= 227 * 1024, "linear_i8: shared memory");
 constexpr int kThreads = 64 + 128 * kGroups;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMaxK = 131072;
 static_assert(kOffBar % 8 == 0 && kOffVec % 16 == 0, "linear_i8: alignment");
 
 struct Geo {
@@ -98,7 +98,7 @@ __device__ __forceinline__ Tile tile_at(int t, const Geo &geo)
 
 // eight (bf16) or four (fp32) outputs, one 16-byte chunk of a staging tile: `acc` scaled, plus
 // the bias (`vec`: the columns' w_scale, their bias 128 floats on) and the addend that `stg` holds
-template <bool F32>
+template <bool F32, bool TOP>
 __device__ __forceinline__ uint4 finish(const uint32_t *acc, float xs, const float *vec, const Geo &geo, const uint4 *stg)
 {
     constexpr int kCols = F32 ? 4 : 8;
@@ -106,10 +106,10 @@ __device__ __forceinline__ uint4 finish(const uint32_t *acc, float xs, const flo
 #pragma unroll
     for (int q = 0; q < kCols / 4; ++q) {
         const float4 ws = *reinterpret_cast<const float4 *>(vec + 4 * q);
-        v[4 * q] = (float)(int)acc[4 * q] * xs * ws.x;
-        v[4 * q + 1] = (float)(int)acc[4 * q + 1] * xs * ws.y;
-        v[4 * q + 2] = (float)(int)acc[4 * q + 2] * xs * ws.z;
-        v[4 * q + 3] = (float)(int)acc[4 * q + 3] * xs * ws.w;
+        v[4 * q] = tc::i8_sum<TOP>(acc[4 * q]) * xs * ws.x;
+        v[4 * q + 1] = tc::i8_sum<TOP>(acc[4 * q + 1]) * xs * ws.y;
+        v[4 * q + 2] = tc::i8_sum<TOP>(acc[4 * q + 2]) * xs * ws.z;
+        v[4 * q + 3] = tc::i8_sum<TOP>(acc[4 * q + 3]) * xs * ws.w;
         if (geo.bias) {
             const float4 b = *reinterpret_cast<const float4 *>(vec + 128 + 4 * q);
             v[4 * q] += b.x, v[4 * q + 1] += b.y, v[4 * q + 2] += b.z, v[4 * q + 3] += b.w;
@@ -149,7 +149,8 @@ template <int OUT_COLS> struct Chunks {
     }
 };
 
-template <bool F32>
+// TOP: K == tc::kI8MaxK
+template <bool F32, bool TOP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_i8_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mb,
                      const __grid_constant__ CUtensorMap mo, const __grid_constant__ CUtensorMap md,
@@ -348,7 +349,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 for (int q = 0; q < 8; ++q) {
                     uint4 *to = reinterpret_cast<uint4 *>(stg + tc::sw128(row, q));
                     // columns past N hold zeros and are not written
-                    *to = finish<F32>(&v[i][q * (kOutCols / 8) / 32][q * (kOutCols / 8) % 32], xs, cv + q * (kOutCols / 8), geo, to);
+                    *to = finish<F32, TOP>(&v[i][q * (kOutCols / 8) / 32][q * (kOutCols / 8) % 32], xs, cv + q * (kOutCols / 8), geo, to);
                 }
                 tc::fence_proxy_async_smem();
                 tc::named_sync(1 + g, 128);
@@ -394,7 +395,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 bool linear_i8_supported(const LinearI8Args &a)
 {
     constexpr int kMost = 0x7fffffff - 1023;  // a tile may reach past the last row or column
-    return a.M > 0 && a.N > 0 && a.M <= kMost && a.N <= kMost && a.K > 0 && a.K % 16 == 0 && a.K <= kMaxK && a.N % 8 == 0 &&
+    return a.M > 0 && a.N > 0 && a.M <= kMost && a.N <= kMost && a.K > 0 && a.K % 16 == 0 && a.K <= tc::kI8MaxK && a.N % 8 == 0 &&
            ((int64_t)a.M + kBM) * ((int64_t)a.N + kBN) / (kBM * kBN) < ((int64_t)1 << 30);
 }
 
@@ -404,7 +405,8 @@ cudaError_t launch_linear_i8(const LinearI8Args &a, cudaStream_t s)
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&nsm, cudaDevAttrMultiProcessorCount, dev);
     if (!tmap_available()) return cudaErrorNotSupported;
     if (linear_i8_few_wanted(a, nsm)) return launch_linear_i8_few(a, nsm, s);
-    auto kernel = a.out_f32 ? linear_i8_kernel<true> : linear_i8_kernel<false>;
+    auto kernel = a.K < tc::kI8MaxK ? (a.out_f32 ? linear_i8_kernel<true, false> : linear_i8_kernel<false, false>)
+                                    : (a.out_f32 ? linear_i8_kernel<true, true> : linear_i8_kernel<false, true>);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
     if (e != cudaSuccess) return e;
     const TmapType ot = a.out_f32 ? TmapType::f32 : TmapType::bf16;

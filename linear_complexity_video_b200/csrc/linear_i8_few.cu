@@ -49,7 +49,8 @@ template <int NT> struct Few {
     static_assert(2 * (kSmem + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
-template <int NT, bool F32>
+// TOP: K == tc::kI8MaxK
+template <int NT, bool F32, bool TOP>
 __global__ void __launch_bounds__(kThreads, 2)
     linear_i8_few_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
                          const __grid_constant__ FewGeo geo, int splits, int *err)
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc::mbar_wait(acc, 0, err);
     tc::tc_fence_after();
     // channel 32 warp + lane of the partial tile, token by token: [token][channel]
-    int *part = reinterpret_cast<int *>(base);
+    uint32_t *part = reinterpret_cast<uint32_t *>(base);
     __syncthreads();
 #pragma unroll
     for (int c = 0; c < NT; c += 16) {
@@ -130,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         tc::tmem_ld16(tc::tmem_addr(tmem, 32 * warp, c), v);
         tc::tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) part[(c + i) * kBC + tid] = (int)v[i];
+        for (int i = 0; i < 16; ++i) part[(c + i) * kBC + tid] = v[i];
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -142,10 +143,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int p = rank * pieces + tid; p < (rank + 1) * pieces; p += kThreads) {
         const int token = p / (kBC / 8), n = c0 + p % (kBC / 8) * 8, m = m0 + token;
         if (m >= geo.M || n >= geo.N) continue;  // N is a multiple of 8
-        const int *at = part + token * kBC + p % (kBC / 8) * 8;
-        int4 a = *reinterpret_cast<const int4 *>(at), b = *reinterpret_cast<const int4 *>(at + 4);
+        const uint32_t *at = part + token * kBC + p % (kBC / 8) * 8;
+        uint4 a = *reinterpret_cast<const uint4 *>(at), b = *reinterpret_cast<const uint4 *>(at + 4);
         // the other CTAs' partial tiles, their loads all in flight at once
-        int4 u[3], w[3];
+        uint4 u[3], w[3];
 #pragma unroll
         for (int i = 1; i < 4; ++i)
             if (i < splits) {
@@ -161,8 +162,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float xs = geo.x_scale[m];
         const float4 wa = *reinterpret_cast<const float4 *>(geo.w_scale + n);
         const float4 wb = *reinterpret_cast<const float4 *>(geo.w_scale + n + 4);
-        float v[8] = {(float)a.x * xs * wa.x, (float)a.y * xs * wa.y, (float)a.z * xs * wa.z, (float)a.w * xs * wa.w,
-                      (float)b.x * xs * wb.x, (float)b.y * xs * wb.y, (float)b.z * xs * wb.z, (float)b.w * xs * wb.w};
+        auto sum = [](uint32_t acc) { return tc::i8_sum<TOP>(acc); };
+        float v[8] = {sum(a.x) * xs * wa.x, sum(a.y) * xs * wa.y, sum(a.z) * xs * wa.z, sum(a.w) * xs * wa.w,
+                      sum(b.x) * xs * wb.x, sum(b.y) * xs * wb.y, sum(b.z) * xs * wb.z, sum(b.w) * xs * wb.w};
         if (geo.bias) {
             const float4 ba = *reinterpret_cast<const float4 *>(geo.bias + n);
             const float4 bb = *reinterpret_cast<const float4 *>(geo.bias + n + 4);
@@ -201,7 +203,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 template <int NT> cudaError_t launch(const LinearI8Args &a, int nsm, cudaStream_t s)
 {
-    auto kernel = a.out_f32 ? linear_i8_few_kernel<NT, true> : linear_i8_few_kernel<NT, false>;
+    auto kernel = a.K < tc::kI8MaxK ? (a.out_f32 ? linear_i8_few_kernel<NT, true, false> : linear_i8_few_kernel<NT, false, false>)
+                                    : (a.out_f32 ? linear_i8_few_kernel<NT, true, true> : linear_i8_few_kernel<NT, false, true>);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Few<NT>::kSmem);
     if (e != cudaSuccess) return e;
     CUtensorMap mx, mw;

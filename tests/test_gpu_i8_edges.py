@@ -94,3 +94,22 @@ def test_sizes_past_32_bits_are_refused():
             call()
     del long
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(3, 16, 131072), (3, 16, 131056), (1088, 2304, 131072)])
+def test_codes_of_minus_128(M, N, K, dtype):
+    """The codes that quantise_rows never writes, -128, are exact too: 128 * 128 * 131,072 is 2^31. Rows of
+    both kernels (the last shape is the pairs'): all -128; one code off; all 127 against it."""
+    x = torch.full((M, K), -128, dtype=torch.int8, device="cuda")
+    w = torch.full((N, K), -128, dtype=torch.int8, device="cuda")
+    x[1, K - 1], x[2], w[5] = -127, 127, 127
+    one = lambda n: torch.ones(n, device="cuda")  # noqa: E731
+    got = mate.linear_i8(x, one(M), w, one(N), out_dtype=dtype).cpu()
+    want = torch.full((M, N), 128.0 * 128 * K, dtype=torch.float64)
+    want[1] -= 128
+    want[2] = -128.0 * 127 * K
+    want[:, 5] = -128.0 * 127 * K
+    want[1, 5] += 127
+    want[2, 5] = 127.0 * 127 * K
+    assert torch.equal(got, want.float().to(dtype))
