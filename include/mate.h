@@ -472,9 +472,10 @@ int mate_frontend_fwd(const void *u, const void *w_in, const float *conv_w, cons
  * rounded to bf16 as there).
  *   u    : (batch, T, H, W, d_model) int8;  u_scale : (batch, T, H, W) fp32
  *   w_in : (d_inner + dc + nheads, d_model) int8;  w_scale : (d_inner + dc + nheads) fp32
- * u and w_in 16-byte aligned, u_scale 4-byte and w_scale 16-byte aligned; d_inner, dc and nheads
- * multiples of 8, d_model a multiple of 64. All else (dims with dtype MATE_BF16, the storage
- * of the outputs; workspace; returns) as for mate_frontend_fwd.
+ * u and w_in 16-byte aligned, u_scale 4-byte and w_scale 16-byte aligned; d_inner, dc and
+ * nheads multiples of 8, d_model a multiple of 64, at most 131072 (as in mate_linear_i8_fwd).
+ * All else (dims with dtype MATE_BF16, the storage of the outputs; workspace; returns) as for
+ * mate_frontend_fwd.
  */
 int mate_frontend_i8_fwd(const int8_t *u, const float *u_scale, const int8_t *w_in, const float *w_scale,
                          const float *conv_w, const float *conv_b, const float *dt_bias, int T, int H, int W,

@@ -632,8 +632,15 @@ int mate_frontend_i8_fwd(const int8_t *u, const float *u_scale, const int8_t *w_
     size_t pre = 0, total = 0;
     const int rc = front_shape(T, H, W, scan_mode, d, a, pre, total);
     if (rc != MATE_OK) return rc;
-    // the three products write rows of their own scales and outputs from 16-byte boundaries
-    if (a.d_inner % 8) return MATE_ERR_UNSUPPORTED;
+    // each of the three products is one that mate_linear_i8_fwd would take (the sum's length, and rows of
+    // scales and outputs from 16-byte boundaries)
+    LinearI8Args g = {};
+    g.M = a.batch * a.N;
+    g.K = a.d_model;
+    for (int n : {a.d_inner, a.dc, a.nh}) {
+        g.N = n;
+        if (!linear_i8_supported(g)) return MATE_ERR_UNSUPPORTED;
+    }
     if (!u_scale || !w_scale || !aligned(u_scale, 4) || !aligned(w_scale, 16)) return MATE_ERR_INVALID_ARG;
     return frontend_call(u, u_scale, w_in, w_scale, conv_w, conv_b, dt_bias, T, H, W, scan_mode, z, x, dt, B, C, d,
                          workspace, ws_bytes, stream);

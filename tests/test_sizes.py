@@ -40,3 +40,14 @@ def test_entry_point_integers():
     with pytest.raises(ValueError, match="does not fit"):
         api.mate_bissd_workspace_bytes(8, 16, 16, (2 ** 32 + 4, 4, 4), d)
     assert _lib.Int.from_param(ctypes.c_int(5)).value == 5
+
+
+@pytest.mark.parametrize("d_model,want", [(131072, _lib.MATE_ERR_INVALID_ARG), (131136, _lib.MATE_ERR_UNSUPPORTED),
+                                          (1 << 24, _lib.MATE_ERR_UNSUPPORTED)])
+def test_frontend_i8_takes_no_longer_sums_than_the_linear_layer(d_model, want):
+    """int32 holds sums of 131,072 products of codes: the front-end's in_proj has that limit too. (The
+    call that is in bounds is refused for its null pointers, behind the check of its sizes.)"""
+    L, d = mate.load(), _lib.mate_frontend_dims(1, d_model, 8, 64, 1, 64, _lib.MATE_BF16)
+    null = ctypes.c_void_p(0)
+    got = L.mate_frontend_i8_fwd(*[null] * 7, 4, 8, 8, 0, *[null] * 5, ctypes.byref(d), null, 0, null)
+    assert got == want
