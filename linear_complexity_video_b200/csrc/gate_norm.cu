@@ -102,13 +102,14 @@ __global__ void __launch_bounds__(kGnThreads) gate_norm_kernel(GateNormArgs a)
 // row's loads in flight meanwhile: persistent CTAs, and the packed vectors of a row are used
 // up before its sums are.
 
-// y SiLU(z) on pairs: y z / (1 + 2^(-z log2 e)), each exponential and reciprocal one
-// hardware approximation (2 and 1 fp32 steps)
+// y SiLU(z) on pairs: y (z / (1 + 2^(-z log2 e))), each exponential and reciprocal one
+// hardware approximation (2 and 1 fp32 steps). In this order a large y meets a gate that has
+// gone to zero, not the infinity of y z.
 __device__ __forceinline__ float2 gated(float2 y, float2 z)
 {
     const float2 x = tc::mul_f32x2(z, make_float2(-1.44269504f, -1.44269504f));
     const float2 d = tc::add_f32x2(make_float2(tc::ex2_approx(x.x), tc::ex2_approx(x.y)), make_float2(1.f, 1.f));
-    return tc::mul_f32x2(tc::mul_f32x2(y, z), make_float2(tc::rcp_approx(d.x), tc::rcp_approx(d.y)));
+    return tc::mul_f32x2(y, tc::mul_f32x2(z, make_float2(tc::rcp_approx(d.x), tc::rcp_approx(d.y))));
 }
 
 // ONE: the row is one group, whose sum needs one barrier instead of two.

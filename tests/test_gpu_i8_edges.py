@@ -113,3 +113,57 @@ def test_codes_of_minus_128(M, N, K, dtype):
     want[1, 5] += 127
     want[2, 5] = 127.0 * 127 * K
     assert torch.equal(got, want.float().to(dtype))
+
+
+def _gated_bound(y, z):
+    """y SiLU(z) in float64 and how far the kernel's may be from it, u = 2^-24. -z log2 e is off by 2 u of
+    itself (its constant and its product), so 2^that by 2 u |z|, and by 4 u more for the approximation (2
+    steps); the sum's rounding, the reciprocal (one step, 2 u) and the two products add 5 u:
+    9 u + 2 u |z|. The reciprocal of d > 2^126 is flushed to zero, and with it at most |y z| 2^-126."""
+    y, z = y.double().numpy(), z.double().numpy()
+    with np.errstate(over="ignore"):
+        v = y * (z / (1 + np.exp(-z)))
+    return v, np.abs(v) * plain64.U * (9 + 2 * np.abs(z)) + np.abs(y * z) * 2.0 ** -126
+
+
+@pytest.mark.parametrize("M,C,group,spread", [(40, 256, 256, 10), (40, 1032, 344, 30), (33, 5120, 2560, 100),
+                                              (25, 64, 16, 1000)])
+def test_gate_norm_i8_gates_far_from_zero(M, C, group, spread):
+    """Gates of either sign up to several times `spread`: SiLU from 0 (with 2^(-z log2 e) infinite below -88)
+    to z itself."""
+    g = torch.Generator().manual_seed(C)
+    y = torch.randn(M, C, generator=g).to(torch.bfloat16)
+    z = (torch.randn(M, C, generator=g) * spread).to(torch.bfloat16)
+    z[:, ::7] = torch.linspace(-95, -80, z[:, ::7].numel()).to(torch.bfloat16).view(z[:, ::7].shape)
+    w = 1 + torch.randn(C, generator=g) / 10
+    got = mate.gate_norm_i8(y.cuda(), z.cuda(), w.cuda(), group, 1e-5)
+    v, dv = (t.reshape(M, C // group, group) for t in _gated_bound(y, z))
+    N, dN = (t.reshape(M, C) for t in plain64.norm(v, "rms", 1e-5, dv))
+    w = w.double().numpy()
+    plain64.check_codes(host64(got.q), host64(got.scale), N * w, np.abs(w) * dN + 3 * plain64.U * np.abs(N * w))
+
+
+def test_gate_norm_i8_large_values_behind_closed_gates():
+    """|y z| past fp32's largest where SiLU(z) is 0: the value is 0, as in the bf16 kernel, and the row's
+    other values stand. Infinite gates: SiLU(inf) = inf and SiLU(-inf) = -inf * 0, not a number."""
+    inf = float("inf")
+    y, z = (torch.ones(6, 64, dtype=torch.bfloat16) for _ in range(2))
+    y[0, 3], z[0, 3] = 1e20, -1e20
+    y[1, 60], z[1, 60] = -3e38, -200.0
+    y[2, ::2], z[2, ::2] = 1e30, -1e10
+    z[3, 5] = inf
+    z[4, 5] = -inf
+    for group in (64, 32):
+        got = mate.gate_norm_i8(y.cuda(), z.cuda(), torch.ones(64).cuda(), group)
+        plain = mate.gate_norm(y.cuda(), z.cuda(), torch.ones(64).cuda(), group)
+        q, s, p = host64(got.q), host64(got.scale), host64(plain)
+        # each value is 0 or SiLU(1), over the rms of its group (no code is near a border)
+        v = np.where((y == 1).numpy(), 1 / (1 + np.exp(-1.0)), 0.0)[[0, 1, 2, 5]]
+        N = plain64.norm(v.reshape(4, -1, group), "rms", 1e-5)[0].reshape(4, 64)
+        want, scale = plain64.codes(N)
+        fine = [0, 1, 2, 5]
+        assert np.array_equal(q[fine], want)
+        assert (np.abs(s[fine] - scale) <= 2.0 ** -18 * scale).all()
+        assert (np.abs(p[fine] - N) <= (2.0 ** -8 + 2.0 ** -18) * N).all()
+        assert np.isnan(s[3:5]).all() and (q[3:5] == 0).all()
+        assert np.isnan(p[3:5]).any(1).all()
