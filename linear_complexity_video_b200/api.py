@@ -575,12 +575,14 @@ def stack(x, layers, *, norm: str = "rms", residual_scale: float = 1.0, norm_eps
     w_pre and w_post (d_model,) fp32 where the norms have weights; mod (batch, 3 d_model) fp32, the
     shift, scale and gate of every batch element (see modulation()); overrides a dict of block()
     arguments of that layer alone (scan_mode and shift alternate between layers). spec: block()'s
-    arguments. The norm after a layer and the one before the next are one pass. Returns x."""
+    arguments (but for keep, and the stream is the stack's). The norm after a layer and the one before the next are one pass. Returns x."""
     layers = [tuple(ly) + ({},) * (3 - len(ly)) for ly in layers]
     if not layers:
         return x
     C = int(x.shape[-1])
-    for _, mod, _ in layers:
+    for _, mod, over in layers:
+        if "keep" in spec or "keep" in over or "stream" in over:
+            raise ValueError("stack() keeps no layer's intermediate tensors (keep) and has one stream for all layers")
         if tuple(mod.shape) != (x.shape[0], 3 * C):
             raise ValueError(f"mod must be (batch, 3 d_model) = {(int(x.shape[0]), 3 * C)}, got {tuple(mod.shape)}")
     kw = dict(norm=norm, eps=norm_eps)
