@@ -167,3 +167,96 @@ def test_gate_norm_i8_large_values_behind_closed_gates():
         assert (np.abs(p[fine] - N) <= (2.0 ** -8 + 2.0 ** -18) * N).all()
         assert np.isnan(s[3:5]).all() and (q[3:5] == 0).all()
         assert np.isnan(p[3:5]).any(1).all()
+
+
+def test_linear_i8_refusals_on_the_device_by_their_code():
+    """Calls that only the C entry refuses, each otherwise in order, by the code it gives; and what they
+    would have written is as it was."""
+    g = _gen(0)
+    x = torch.randint(-127, 128, (8, 64), generator=g, dtype=torch.int8, device="cuda")
+    w = torch.randint(-127, 128, (8, 64), generator=g, dtype=torch.int8, device="cuda")
+    xs, ws = torch.ones(8, device="cuda"), torch.ones(8, device="cuda")
+    out = torch.full((8, 8), 3.0, dtype=torch.bfloat16, device="cuda")
+    assert mate.linear_i8(x, xs, w, ws, out=out) is out
+    out.fill_(3.0)
+    over = lambda t: t.view(torch.bfloat16).flatten()[:64].view(8, 8)  # noqa: E731  (the first 128 bytes of t)
+    off = torch.zeros(8 * 64 + 8, dtype=torch.int8, device="cuda")[8:].view(8, 64)
+    keep = [t.clone() for t in (x, w, out)]
+    for args, kw, code in (((x, xs, w, ws), dict(out=over(x)), "INVALID_ARG"),
+                           ((x, xs, w, ws), dict(out=over(w)), "INVALID_ARG"),
+                           ((x, xs, w, ws), dict(out=out, addend=torch.ones(9, 8, dtype=torch.bfloat16, device="cuda")[1:]), None),
+                           ((off, xs, w, ws), dict(out=out), "INVALID_ARG"),
+                           ((x, xs, off, ws), dict(out=out), "INVALID_ARG"),
+                           ((x[:0], xs[:0], w, ws), {}, "INVALID_ARG"),
+                           ((x, xs, w[:0], ws[:0]), {}, "INVALID_ARG"),
+                           ((x[:, :0].contiguous(), xs, w[:, :0].contiguous(), ws), dict(out=out), "INVALID_ARG"),
+                           ((x[:, :24].contiguous(), xs, w[:, :24].contiguous(), ws), dict(out=out), "UNSUPPORTED"),
+                           ((x, xs, w[:4], ws[:4]), {}, "UNSUPPORTED")):
+        if code is None:  # the rows of a wider tensor start on their 16 bytes: taken
+            mate.linear_i8(*args, **kw)
+            out.fill_(3.0)
+            continue
+        with pytest.raises(mate.MateError) as e:
+            mate.linear_i8(*args, **kw)
+        assert e.value.code == getattr(mate._lib, "MATE_ERR_" + code)
+    with pytest.raises(ValueError, match="must have shape"):
+        mate.linear_i8(x, xs, w, ws, out=out[:4])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(keep, (x, w, out)))
+    for call, code in ((lambda: mate.quantize_rows(x[:0].to(torch.bfloat16)), "INVALID_ARG"),
+                       (lambda: mate.quantize_rows(x[:, :60].to(torch.bfloat16).contiguous()), "UNSUPPORTED")):
+        with pytest.raises(mate.MateError) as e:
+            call()
+        assert e.value.code == getattr(mate._lib, "MATE_ERR_" + code)
+
+
+@pytest.mark.parametrize("M", [300, 9001])
+def test_products_behind_copies_fills_and_other_streams(M):
+    """Products are launched so that they set themselves up under the call ahead of them. Here that call is
+    a copy, a fill, a torch kernel, or ends on another stream (a fork and a join), eager and captured."""
+    g = _gen(M)
+    codes = lambda *s: torch.randint(-127, 128, s, generator=g, dtype=torch.int8, device="cuda")  # noqa: E731
+    x0, x1, w = codes(M, 256), codes(M, 256), codes(520, 256)
+    xs, ws = torch.rand(M, generator=g, device="cuda"), torch.rand(520, generator=g, device="cuda")
+    x = torch.empty_like(x0)
+    s2 = torch.empty_like(xs)
+    outs = [torch.empty(M, 520, dtype=torch.float32, device="cuda") for _ in range(5)]
+    side = torch.cuda.Stream()
+    lin = lambda out, scale=xs, **kw: mate.linear_i8(x, scale, w, ws, out_dtype=torch.float32, out=out, **kw)  # noqa: E731
+
+    def run():
+        x.copy_(x0)                       # a copy
+        lin(outs[0])
+        x.zero_()                         # a fill
+        lin(outs[1])
+        torch.add(x0, 0, out=x)           # a torch kernel
+        torch.mul(xs, 2, out=s2)
+        lin(outs[2], s2)
+        torch.mul(xs, 3, out=s2)          # two kernels on two streams, joined
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            x.copy_(x1)
+            lin(outs[3])                  # and a product on the side stream ahead of the join
+        main.wait_stream(side)
+        lin(outs[4], s2, addend=outs[3])
+
+    def check():
+        torch.cuda.synchronize()
+        dot = lambda a, s: mate.linear_i8(a, s, w, ws, out_dtype=torch.float32)  # noqa: E731
+        assert torch.equal(outs[0], dot(x0, xs)) and (outs[1] == 0).all()
+        assert torch.equal(outs[2], dot(x0, 2 * xs)) and torch.equal(outs[3], dot(x1, xs))
+        assert torch.equal(outs[4], mate.linear_i8(x1, 3 * xs, w, ws, out_dtype=torch.float32, addend=outs[3]))
+        assert mate.mate_last_error() == 0
+
+    for _ in range(3):
+        run()
+        check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(5):
+        for o in (x, s2, *outs):
+            o.zero_()
+        graph.replay()
+        check()
