@@ -339,7 +339,8 @@ typedef struct {
  * with an exact sum (of any int8 codes, -128 among them), scales, bias and addend in
  * fp32, one rounding to the output type. The addend serves an output that is the sum
  * of products whose inputs have scales of their own (the MATE composition of two
- * branches).
+ * branches). x_scale is applied before w_scale: a sum times x_scale above 3.4e38 is
+ * infinite, however small w_scale is.
  *   x       : (tokens, k) int8, row-major;  x_scale : (tokens) fp32
  *   w       : (n, k)      int8, row-major;  w_scale : (n)      fp32
  *   bias    : (n) fp32 or NULL
@@ -409,7 +410,8 @@ typedef struct {
  * x, y, x_out and h 16-byte aligned, fp32 vectors 4-byte aligned. channels a
  * multiple of 8, at most 8192; batch * tokens at most 2^30; eps >= 0 and finite;
  * residual_scale finite; strides >= 0. Squares are summed in fp32, so magnitudes
- * above about 1e18 overflow them. Results are bitwise reproducible. Returns
+ * above about 1e18 overflow them (N is 0 there), and with eps = 0 rows of magnitudes
+ * below about 1e-19 underflow them (N is not finite). Results are bitwise reproducible. Returns
  * MATE_OK, MATE_ERR_INVALID_ARG (bad pointers, sizes, eps, strides, combinations
  * or overlap), MATE_ERR_UNSUPPORTED (other dtypes, norms or sizes) or
  * MATE_ERR_CUDA.

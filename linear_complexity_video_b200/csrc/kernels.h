@@ -161,7 +161,7 @@ struct BlockNormArgs {
     int batch, n, C;
     int post, pre;           // MATE_NORM_*
     int x_f32;
-    int h_type;              // MATE_BF16, MATE_F32 or MATE_I8
+    int h_type;              // MATE_BF16 or MATE_I8
     int64_t gate_stride, scale_stride, shift_stride;
     float alpha, eps;
 };

@@ -23,12 +23,17 @@
 //             (read from global memory chunk by chunk they cost in_proj of 131,072
 //             tokens 3.20 ms instead of 2.48). One group instead of two: 15.4 us
 //             instead of 12.8 for 1,155 tokens, 2,560 -> 2,560.
-// What bounds it: with its operands in place an MMA takes about 146 cycles (128 nominal,
-// and as long at N = 192 or 128, so a narrower tile gains nothing: 4,096 tokens, 2,560 ->
-// 2,560, take 30 us in 256 columns and 39 in 128); a K step of four takes 0.30 us, 0.33 with
-// its loads, and 0.37 to 0.39 in runs of a few hundred microseconds and more, where the
-// board's power limit lowers the clocks (2,450 to 2,800 TOP/s, 0.9 to 1.0 of twice the sustained
-// bf16 rate; 2,890 to 3,300 in single cold launches). Tried and left: a ring of six stages (no
+// What bounds it: the MMAs, at the clock that the board's power limit leaves. The four of a K
+// step are 512 cycles nominal and 584 with their operands in place. At 1,965 MHz a K step takes
+// 0.33 us = 648 cycles (1,155 tokens -> 2,560 in a graph: 13.3 us at K = 2,560, 7.0 at K = 128).
+// In loops of seconds, by the time of a call over the K steps that a pair takes one after another
+// and the clock sampled meanwhile: 0.43 us = 596 cycles of 1,387 MHz (32,768 tokens, 7,680 ->
+// 2,560: 2,780 TOP/s), 0.48 us = 648 cycles of 1,357 MHz (in_proj of 131,072 tokens: 2,590 TOP/s,
+// 0.94 of twice the sustained bf16 rate), 0.48 us = 682 cycles of 1,425 MHz (32,768 tokens,
+// 2,560 -> 2,560: 2,490, the unfilled last round of tiles counted in). Single launches after a
+// pause, at a higher clock: 3,210, 2,940 and 2,610 TOP/s. Tiles of 192 and 128 columns lost as
+// whole kernels (4,096 tokens, 2,560 -> 2,560: 39 us in 128 columns, 30 in 256); what share of
+// that is the MMAs' and what the loads' was not told apart. Tried and left: a ring of six stages (no
 // change); tiles of 256 x 512 with x loaded once for both halves (a quarter less to load: 476 us
 // against 492 for 32,768 tokens, 7,680 -> 2,560, but 181 against 175 at K = 2,560, since one tile
 // fills TMEM and its epilogue is exposed).

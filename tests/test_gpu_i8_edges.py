@@ -260,3 +260,31 @@ def test_products_behind_copies_fills_and_other_streams(M):
             o.zero_()
         graph.replay()
         check()
+
+
+@pytest.mark.slow
+def test_offsets_past_32_bits():
+    """More than 2^32 elements in a call: sampled rows, the last ones among them, against the same rows alone."""
+    M, C = 2 ** 20 + 3, 4104
+    rows = torch.tensor([0, 1, 2 ** 19 - 1, 2 ** 19 + 5, M - 2, M - 1], device="cuda")
+    g = _gen(1)
+    x = torch.empty(M, C, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    z = torch.empty_like(x).normal_(generator=g)
+    w = torch.rand(C, generator=g, device="cuda") + 0.5
+    a, b = mate.quantize_rows(x), mate.quantize_rows(x[rows])
+    assert torch.equal(a.q[rows], b.q) and torch.equal(a.scale[rows], b.scale)
+    a, b = mate.gate_norm_i8(x, z, w, 1368), mate.gate_norm_i8(x[rows], z[rows], w, 1368)
+    assert torch.equal(a.q[rows], b.q) and torch.equal(a.scale[rows], b.scale)
+    (r, h), (rr, hh) = (mate.block_norm(u[None], v[None], w_post=w, h_dtype=torch.int8) for u, v in ((x, z), (x[rows], z[rows])))
+    assert torch.equal(r[0, rows], rr[0]) and torch.equal(h.q[0, rows], hh.q[0]) and torch.equal(h.scale[0, rows], hh.scale[0])
+    del x, z, a, r, h
+    K = 64
+    q = torch.randint(-127, 128, (M, K), generator=g, dtype=torch.int8, device="cuda")
+    wq = torch.randint(-127, 128, (C, K), generator=g, dtype=torch.int8, device="cuda")
+    s = torch.rand(M, generator=g, device="cuda")
+    out = mate.linear_i8(q, s, wq, w)
+    assert torch.equal(out[rows], mate.linear_i8(q[rows], s[rows], wq, w))
+    assert torch.equal(mate.linear_i8(q, s, wq, w, addend=out, out=out)[rows], mate.linear_i8(q[rows], s[rows], wq, w, addend=mate.linear_i8(q[rows], s[rows], wq, w)))
+    del out
+    torch.cuda.empty_cache()
+    assert mate.mate_last_error() == 0
