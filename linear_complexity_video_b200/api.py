@@ -53,6 +53,17 @@ def _require(t: torch.Tensor, name: str, dtype=None):
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
 
 
+def _holds(t: torch.Tensor, name: str, n: int):
+    """A tensor holds the `n` elements that the call reads or writes through its address."""
+    if t.numel() < n:
+        raise ValueError(f"{name} must hold {n} elements, got {tuple(t.shape)}")
+
+
+def _matrix(w: torch.Tensor, name: str, rows: int, cols: int):
+    if w.numel() != rows * cols:
+        raise ValueError(f"{name} must be ({rows}, {cols}), got {tuple(w.shape)}")
+
+
 class Codes(NamedTuple):
     """Rows held as 8-bit codes: value[..., k] is about q[..., k] * scale[...]."""
     q: torch.Tensor      # (..., K) int8
@@ -228,8 +239,15 @@ def bissd(x, dt, A, B, C, D, scan_mode: int, review_pool=None, chunk: int = 256,
         _require(t, n, torch.float32)
     b, T, H, W, nh, P = x.shape
     G, Ns = B.shape[4:]
+    tokens = b * T * H * W
+    for t, n, size in ((dt, "dt", tokens * nh), (A, "A", nh), (D, "D", nh), (B, "B", tokens * G * Ns),
+                       (C, "C", tokens * G * Ns)):
+        _holds(t, n, size)
     if out is None:
         out = torch.empty_like(x)
+    else:
+        _require(out, "out", x.dtype)
+        _holds(out, "out", x.numel())
     if workspace is None:
         workspace = bissd_workspace(x, B, review_pool, chunk, directions)
     dims = ssd_dims(b, nh, P, Ns, G, chunk, x.dtype, directions)
@@ -242,8 +260,13 @@ def tesa(q, k, v, Tw: int, Sw: int, shift=(0, 0, 0), out: Optional[torch.Tensor]
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         _require(t, n, q.dtype)
     b, T, H, W, nh, d = q.shape
+    _holds(k, "k", q.numel())
+    _holds(v, "v", q.numel())
     if out is None:
         out = torch.empty_like(q)
+    else:
+        _require(out, "out", q.dtype)
+        _holds(out, "out", q.numel())
     tesa_fwd(q, k, v, T, H, W, Tw, Sw, shift, out, attn_dims(b, nh, d, q.dtype), stream)
     return out
 
@@ -261,8 +284,13 @@ def compose(y_ma, y_te, w_ma, w_te, out: Optional[torch.Tensor] = None, stream=N
     for s in lead:
         M *= int(s)
     N = int(w_ma.shape[0])
+    _matrix(w_ma, "w_ma", N, int(y_ma.shape[-1]))
+    _matrix(w_te, "w_te", N, int(y_te.shape[-1]))
     if out is None:
         out = torch.empty(*lead, N, dtype=torch.bfloat16, device=y_ma.device)
+    else:
+        _require(out, "out", torch.bfloat16)
+        _holds(out, "out", M * N)
     dims = mate_compose_dims(M, int(y_ma.shape[-1]), int(y_te.shape[-1]), N, MATE_BF16)
     mate_compose_fwd(y_ma, y_te, w_ma, w_te, out, dims, stream)
     return out
@@ -282,6 +310,9 @@ def gate_norm(y, z, w, group: int, eps: float = 1e-5, out: Optional[torch.Tensor
         M *= int(s)
     if out is None:
         out = torch.empty_like(y)
+    else:
+        _require(out, "out", torch.bfloat16)
+        _holds(out, "out", y.numel())
     dims = mate_gate_norm_dims(M, int(y.shape[-1]), int(group), MATE_BF16)
     mate_gate_norm_fwd(y, z, w, eps, out, dims, stream)
     return out
@@ -296,8 +327,12 @@ def linear(x, w, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tenso
     for s in x.shape[:-1]:
         M *= int(s)
     N = int(w.shape[0])
+    _matrix(w, "w", N, int(x.shape[-1]))
     if out is None:
         out = torch.empty(*x.shape[:-1], N, dtype=torch.bfloat16, device=x.device)
+    else:
+        _require(out, "out", torch.bfloat16)
+        _holds(out, "out", M * N)
     mate_compose_fwd(x, None, w, None, out, mate_compose_dims(M, int(x.shape[-1]), 0, N, MATE_BF16), stream)
     return out
 
@@ -624,6 +659,10 @@ def frontend(u, w_in, conv_w, conv_b, dt_bias, scan_mode: int, nheads: int, head
     for t, n in ((conv_w, "conv_w"), (conv_b, "conv_b"), (dt_bias, "dt_bias")):
         _require(t, n, torch.float32)
     b, T, H, W, dm = u.shape
+    dc = nheads * headdim + 2 * ngroups * dstate
+    _matrix(w_in, "w_in", nheads * headdim + dc + nheads, dm)
+    for t, n, size in ((conv_w, "conv_w", dc * 4), (conv_b, "conv_b", dc), (dt_bias, "dt_bias", nheads)):
+        _holds(t, n, size)
     dims = mate_frontend_dims(b, dm, nheads, headdim, ngroups, dstate, MATE_BF16)
     nbytes = mate_frontend_workspace_bytes(T, H, W, dims)
     if nbytes == 0:
